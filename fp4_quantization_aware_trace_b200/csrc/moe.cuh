@@ -1,0 +1,245 @@
+// moe.cuh -- the routing sort, tokens into expert order and back with the
+// routing weights, and their gradients.  Included by trace_fp4.cu inside its
+// anonymous namespace.
+//
+// A slot is one (token, choice) pair, numbered token * k + choice.  The sort
+// gives each slot a row; rows of one expert are contiguous and in slot order
+// (a stable counting sort: no atomic decides an order, so a run repeats bit
+// for bit).  Slots whose expert id is outside [0, E) are dropped: they fill
+// the last group, group E, and carry no row.
+#pragma once
+
+constexpr int kSortMaxWarps = 32;
+constexpr uint32_t kSortSmem = 48u * 1024u;  // per-warp counters: no opt-in needed
+constexpr uint32_t kSortChunk = 4096u;       // slots per CTA; one CTA sorts as many alone
+
+// The counter a slot belongs to: its expert, or E for a dropped one.
+template <typename ID>
+__device__ __forceinline__ uint32_t sort_key(const ID* __restrict__ ids, uint32_t slot,
+                                             uint32_t E) {
+  const ID v = ids[slot];
+  return v >= (ID)0 && (long long)v < (long long)E ? (uint32_t)v : E;
+}
+
+// First pass of a sort over several CTAs: counts of one chunk of slots.
+template <typename ID>
+__global__ void k_moe_count(const ID* __restrict__ ids, uint32_t slots, uint32_t E,
+                            uint32_t* __restrict__ counts) {
+  extern __shared__ uint32_t hist[];
+  pdl_begin();
+  for (uint32_t e = threadIdx.x; e <= E; e += blockDim.x) hist[e] = 0u;
+  __syncthreads();
+  const uint32_t first = blockIdx.x * kSortChunk;
+  const uint32_t last = min(first + kSortChunk, slots);
+  for (uint32_t s = first + threadIdx.x; s < last; s += blockDim.x)
+    atomicAdd(&hist[sort_key(ids, s, E)], 1u);
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e <= E; e += blockDim.x)
+    counts[(size_t)blockIdx.x * (E + 1u) + e] = hist[e];
+}
+
+// Second pass (the only one when a single CTA holds every slot).  Each warp
+// owns a contiguous piece of the CTA's chunk and counts it; the counters
+// then become each warp's next row per expert: rows of earlier experts +
+// this expert's rows in earlier chunks + in earlier warps.  In the last
+// walk the lanes of one expert rank themselves by lane, which is slot order.
+template <typename ID>
+__global__ void __launch_bounds__(32 * kSortMaxWarps)
+    k_moe_place(const ID* __restrict__ ids, uint32_t slots, uint32_t E,
+                const uint32_t* __restrict__ counts, int64_t* __restrict__ offsets,
+                int32_t* __restrict__ rows, int32_t* __restrict__ slot_of) {
+  extern __shared__ uint32_t next[];  // [warps][E + 1]
+  __shared__ uint32_t part[kSortMaxWarps];
+  __shared__ uint32_t carry;
+  const uint32_t n = E + 1u, warps = blockDim.x / 32u;
+  const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
+  pdl_begin();
+  for (uint32_t i = threadIdx.x; i < warps * n; i += blockDim.x) next[i] = 0u;
+  if (threadIdx.x == 0) carry = 0u;
+  __syncthreads();
+  const uint32_t first = blockIdx.x * kSortChunk, last = min(first + kSortChunk, slots);
+  const uint32_t piece = (last - first + warps * 32u - 1u) / (warps * 32u) * 32u;
+  const uint32_t lo = min(first + warp * piece, last), hi = min(lo + piece, last);
+  uint32_t* mine = next + warp * n;
+  for (uint32_t s0 = lo; s0 < hi; s0 += 32u) {
+    const bool in = s0 + lane < hi;
+    const uint32_t e = in ? sort_key(ids, s0 + lane, E) : n;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    if (in && lane == (uint32_t)__ffs((int)same) - 1u) mine[e] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (uint32_t e0 = 0; e0 < n; e0 += blockDim.x) {
+    const uint32_t e = e0 + threadIdx.x;
+    uint32_t total = 0u, before = 0u;
+    if (e < n) {
+      if (counts != nullptr) {
+#pragma unroll 8
+        for (uint32_t c = 0; c < gridDim.x; ++c) {
+          const uint32_t v = counts[(size_t)c * n + e];
+          total += v;
+          before += c < blockIdx.x ? v : 0u;
+        }
+      } else {
+        for (uint32_t w = 0; w < warps; ++w) total += next[w * n + e];
+      }
+    }
+    // exclusive scan of the totals over the CTA
+    uint32_t sum = total;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= (uint32_t)d) sum += v;
+    }
+    if (lane == 31u) part[warp] = sum;
+    __syncthreads();
+    uint32_t base = carry;
+    for (uint32_t w = 0; w < warp; ++w) base += part[w];
+    uint32_t at = base + sum - total;
+    __syncthreads();
+    if (threadIdx.x == blockDim.x - 1u) carry = base + sum;
+    if (e < n) {
+      if (blockIdx.x == 0) offsets[e] = (int64_t)at;
+      at += before;
+      for (uint32_t w = 0; w < warps; ++w) {
+        const uint32_t v = next[w * n + e];
+        next[w * n + e] = at;
+        at += v;
+      }
+    }
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) offsets[n] = (int64_t)slots;
+  for (uint32_t s0 = lo; s0 < hi; s0 += 32u) {
+    const uint32_t s = s0 + lane;
+    const bool in = s < hi;
+    const uint32_t e = in ? sort_key(ids, s, E) : n;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    if (in) {
+      const uint32_t r = mine[e] + __popc(same & ((1u << lane) - 1u));
+      rows[s] = e < E ? (int32_t)r : -1;
+      slot_of[r] = e < E ? (int32_t)s : -1;
+    }
+    __syncwarp();
+    if (in && lane == (uint32_t)__ffs((int)same) - 1u) mine[e] += __popc(same);
+    __syncwarp();
+  }
+}
+
+// The work of one warp in the token kernels: 512 columns (32 bytes per lane)
+// of one token.
+struct MoeShape {
+  uint32_t tokens, k, slots;
+  uint32_t lanes;  // 32-byte words per row
+  uint32_t segs;   // warps per row
+};
+
+// Tokens into expert order: y[rows[t, j]] = x[t], each x word read once;
+// rows without a slot are zeroed by the warp of the token with that number.
+__global__ void __launch_bounds__(kThreads)
+    k_moe_dispatch(const V8* __restrict__ x, MoeShape sh, const int32_t* __restrict__ rows,
+                   const int32_t* __restrict__ slot_of, V8* __restrict__ y) {
+  pdl_begin();
+  const uint32_t lane = threadIdx.x % 32u;
+  const u64 units = (u64)sh.tokens * sh.segs;
+  for (u64 u = (u64)blockIdx.x * (kThreads / 32) + threadIdx.x / 32u; u < units;
+       u += (u64)gridDim.x * (kThreads / 32)) {
+    const uint32_t t = (uint32_t)(u / sh.segs), w = (uint32_t)(u % sh.segs) * 32u + lane;
+    const bool in = w < sh.lanes;
+    const V8 v = in ? ld_block_stream(x + (size_t)t * sh.lanes + w) : zero_block();
+    for (uint32_t j = 0; j < sh.k; ++j) {
+      const uint32_t s = t * sh.k + j;
+      const int32_t r = rows[s];
+      if (in && (uint32_t)r < sh.slots) st_block(y + (size_t)r * sh.lanes + w, v);
+      if (in && slot_of[s] < 0) st_block(y + (size_t)s * sh.lanes + w, zero_block());
+    }
+  }
+}
+
+// Back to token order: out[t] = sum_j weights[t, j] y[rows[t, j]] in fp32, in
+// the order of j, rounded once; weights == NULL sums with weight one (the
+// gradient of dispatch).
+__global__ void __launch_bounds__(kThreads)
+    k_moe_combine(const V8* __restrict__ y, MoeShape sh, const int32_t* __restrict__ rows,
+                  const float* __restrict__ weights, V8* __restrict__ out) {
+  pdl_begin();
+  const uint32_t lane = threadIdx.x % 32u;
+  const u64 units = (u64)sh.tokens * sh.segs;
+  for (u64 u = (u64)blockIdx.x * (kThreads / 32) + threadIdx.x / 32u; u < units;
+       u += (u64)gridDim.x * (kThreads / 32)) {
+    const uint32_t t = (uint32_t)(u / sh.segs), w = (uint32_t)(u % sh.segs) * 32u + lane;
+    if (w >= sh.lanes) continue;
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+    for (uint32_t j0 = 0; j0 < sh.k; j0 += 4u) {
+      V8 v[4];
+      float f[4];
+      bool live[4];
+#pragma unroll
+      for (uint32_t q = 0; q < 4u; ++q) {
+        const uint32_t s = t * sh.k + j0 + q;
+        const int32_t r = j0 + q < sh.k ? rows[s] : -1;
+        live[q] = (uint32_t)r < sh.slots;
+        if (live[q]) {
+          v[q] = ld_block_stream(y + (size_t)r * sh.lanes + w);
+          f[q] = weights != nullptr ? weights[s] : 1.0f;
+        }
+      }
+#pragma unroll
+      for (uint32_t q = 0; q < 4u; ++q) {
+        if (!live[q]) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc[2 * i] = __fmaf_rn(f[q], bf16_lo(v[q].w[i]), acc[2 * i]);
+          acc[2 * i + 1] = __fmaf_rn(f[q], bf16_hi(v[q].w[i]), acc[2 * i + 1]);
+        }
+      }
+    }
+    V8 o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.w[i] = cvt_bf16x2(acc[2 * i], acc[2 * i + 1]);
+    st_block(out + (size_t)t * sh.lanes + w, o);
+  }
+}
+
+// Gradients of combine, one warp per slot (the k slots of a token are
+// neighbours, so its dout row comes from L1 after the first):
+// dy[rows[s]] = weights[s] dout[t], dweights[s] = <dout[t], y[rows[s]]> in
+// fp32 (each lane in column order, then a fixed tree).
+__global__ void __launch_bounds__(kThreads)
+    k_moe_combine_bwd(const V8* __restrict__ dout, const V8* __restrict__ y, MoeShape sh,
+                      const int32_t* __restrict__ rows, const int32_t* __restrict__ slot_of,
+                      const float* __restrict__ weights, V8* __restrict__ dy,
+                      float* __restrict__ dweights) {
+  pdl_begin();
+  const uint32_t lane = threadIdx.x % 32u;
+  for (uint32_t s = blockIdx.x * (kThreads / 32) + threadIdx.x / 32u; s < sh.slots;
+       s += gridDim.x * (kThreads / 32)) {
+    const uint32_t t = s / sh.k;
+    const int32_t r = rows[s];
+    const bool live = (uint32_t)r < sh.slots;
+    float dot = 0.0f;
+    if (live) {
+      const float f = weights[s];
+      for (uint32_t w = lane; w < sh.lanes; w += 32u) {
+        const V8 a = ld_block_l1(dout + (size_t)t * sh.lanes + w);
+        const V8 b = ld_block_stream(y + (size_t)r * sh.lanes + w);
+        V8 o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dot = __fmaf_rn(bf16_lo(a.w[i]), bf16_lo(b.w[i]), dot);
+          dot = __fmaf_rn(bf16_hi(a.w[i]), bf16_hi(b.w[i]), dot);
+          o.w[i] = cvt_bf16x2(f * bf16_lo(a.w[i]), f * bf16_hi(a.w[i]));
+        }
+        st_block(dy + (size_t)r * sh.lanes + w, o);
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+    if (lane == 0) dweights[s] = dot;
+    if (slot_of[s] < 0)
+      for (uint32_t w = lane; w < sh.lanes; w += 32u)
+        st_block(dy + (size_t)s * sh.lanes + w, zero_block());
+  }
+}

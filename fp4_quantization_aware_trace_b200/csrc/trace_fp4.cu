@@ -73,6 +73,8 @@ namespace {
 #include "mx.cuh"
 #include "mismatch.cuh"
 #include "util.cuh"
+#include "moe.cuh"
+#include "matmul.cuh"
 
 // ---------------------------------------------------------------------------
 // Host side
@@ -260,6 +262,35 @@ int coop_grid_for(const Shape& sh, int* grid) {
   if (sh.ntiles < g) g = sh.ntiles;
   *grid = (int)(g > 0 ? g : 1);
   return TRACE_OK;
+}
+
+template <typename ID>
+int moe_sort_launch(const ID* ids, uint32_t slots, uint32_t E, int64_t* offsets,
+                           int32_t* rows, int32_t* slot_of, uint32_t* counts, cudaStream_t s) {
+  const uint32_t chunks = (slots + kSortChunk - 1) / kSortChunk;
+  uint32_t warps = kSortSmem / (4u * (E + 1u));
+  if (warps > (uint32_t)kSortMaxWarps) warps = kSortMaxWarps;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(chunks > 0 ? chunks : 1);
+  if (chunks > 1) {
+    cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = 4u * (E + 1u);
+    if (cudaLaunchKernelEx(&cfg, k_moe_count<ID>, ids, slots, E, counts) != cudaSuccess)
+      return TRACE_ERR_CUDA;
+  }
+  cfg.blockDim = dim3(32u * warps);
+  cfg.dynamicSmemBytes = 4u * warps * (E + 1u);
+  return cudaLaunchKernelEx(&cfg, k_moe_place<ID>, ids, slots, E,
+                            (const uint32_t*)(chunks > 1 ? counts : nullptr), offsets, rows,
+                            slot_of) == cudaSuccess
+             ? TRACE_OK
+             : TRACE_ERR_CUDA;
 }
 
 }  // namespace
@@ -821,6 +852,169 @@ int trace_capture_static_ws(const uint16_t* x, int64_t rows, int64_t cols, int32
   // the array is zeroed by the capture's first kernel on every call
   return capture_impl(x, rows, cols, num_groups, group_row_offsets, codes, mbits, scales, gscale,
                       ws, sizeof(g_capture_scratch), false, stream, true);
+}
+
+// ---------------------------------------------------------------------------
+// FP4 experts: the routing sort, tokens to expert order and back, the product
+// ---------------------------------------------------------------------------
+static int check_slots(int64_t tokens, int64_t k) {
+  if (tokens < 0 || k < 1 || k > 65536 || tokens > ((int64_t)1 << 31) - 1 ||
+      tokens * k > ((int64_t)1 << 31) - 1)
+    return TRACE_ERR_SHAPE;
+  return TRACE_OK;
+}
+
+size_t trace_moe_sort_workspace_bytes(int64_t tokens, int64_t k, int32_t num_experts) {
+  if (check_slots(tokens, k) || num_experts < 1 || num_experts > TRACE_MOE_MAX_EXPERTS) return 0;
+  const uint64_t chunks = ((uint64_t)(tokens * k) + kSortChunk - 1) / kSortChunk;
+  const uint64_t words = chunks > 1 ? chunks * (uint64_t)(num_experts + 1) : 1;
+  return (size_t)((words * 4 + 255) / 256 * 256);
+}
+
+int trace_moe_sort(const void* expert_ids, int32_t id_bytes, int64_t tokens, int64_t k,
+                   int32_t num_experts, int64_t* offsets, int32_t* rows, int32_t* slots,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_slots(tokens, k);
+  if (st) return st;
+  if (num_experts < 1 || num_experts > TRACE_MOE_MAX_EXPERTS || (id_bytes != 4 && id_bytes != 8))
+    return TRACE_ERR_SHAPE;
+  if (!offsets || !workspace || (tokens > 0 && (!expert_ids || !rows || !slots)))
+    return TRACE_ERR_NULL;
+  if (!aligned(expert_ids, (uintptr_t)id_bytes) || !aligned(offsets, 8) || !aligned(rows, 4) ||
+      !aligned(slots, 4) || !aligned(workspace, 256))
+    return TRACE_ERR_ALIGN;
+  if (workspace_bytes < trace_moe_sort_workspace_bytes(tokens, k, num_experts))
+    return TRACE_ERR_WORKSPACE;
+  const uint32_t n = (uint32_t)(tokens * k);
+  if (id_bytes == 4)
+    return moe_sort_launch((const int32_t*)expert_ids, n, (uint32_t)num_experts, offsets, rows,
+                           slots, (uint32_t*)workspace, (cudaStream_t)stream);
+  return moe_sort_launch((const long long*)expert_ids, n, (uint32_t)num_experts, offsets, rows,
+                         slots, (uint32_t*)workspace, (cudaStream_t)stream);
+}
+
+// Shape of the token kernels and the grid for `units` warps of work.
+static int moe_shape(int64_t tokens, int64_t k, int64_t cols, MoeShape* sh) {
+  const int st = check_slots(tokens, k);
+  if (st) return st;
+  if (cols <= 0 || cols % 32 != 0 || cols > ((int64_t)1 << 31) - 32) return TRACE_ERR_SHAPE;
+  sh->tokens = (uint32_t)tokens;
+  sh->k = (uint32_t)k;
+  sh->slots = (uint32_t)(tokens * k);
+  sh->lanes = (uint32_t)(cols / 16);
+  sh->segs = (sh->lanes + 31u) / 32u;
+  return TRACE_OK;
+}
+
+static int moe_grid(u64 units, int* grid) {
+  const int sms = sm_count();
+  if (sms <= 0) return TRACE_ERR_CUDA;
+  const u64 ctas = (units + kThreads / 32 - 1) / (kThreads / 32);
+  const u64 most = (u64)sms * kGridPerSm;
+  *grid = (int)(ctas < most ? ctas : most);
+  return TRACE_OK;
+}
+
+int trace_moe_dispatch(const uint16_t* x, int64_t tokens, int64_t k, int64_t cols,
+                       const int32_t* rows, const int32_t* slots, uint16_t* y, void* stream) {
+  MoeShape sh;
+  int st = moe_shape(tokens, k, cols, &sh), grid;
+  if (st) return st;
+  if (tokens == 0) return TRACE_OK;
+  if (!x || !rows || !slots || !y) return TRACE_ERR_NULL;
+  if (!aligned(x, 32) || !aligned(rows, 4) || !aligned(slots, 4) || !aligned(y, 32))
+    return TRACE_ERR_ALIGN;
+  if ((st = moe_grid((u64)sh.tokens * sh.segs, &grid))) return st;
+  return launch(k_moe_dispatch, grid, (cudaStream_t)stream, (const V8*)x, sh, rows, slots, (V8*)y);
+}
+
+int trace_moe_combine(const uint16_t* y, int64_t tokens, int64_t k, int64_t cols,
+                      const int32_t* rows, const float* weights, uint16_t* out, void* stream) {
+  MoeShape sh;
+  int st = moe_shape(tokens, k, cols, &sh), grid;
+  if (st) return st;
+  if (tokens == 0) return TRACE_OK;
+  if (!y || !rows || !out) return TRACE_ERR_NULL;
+  if (!aligned(y, 32) || !aligned(rows, 4) || !aligned(weights, 4) || !aligned(out, 32))
+    return TRACE_ERR_ALIGN;
+  if ((st = moe_grid((u64)sh.tokens * sh.segs, &grid))) return st;
+  return launch(k_moe_combine, grid, (cudaStream_t)stream, (const V8*)y, sh, rows, weights,
+                (V8*)out);
+}
+
+int trace_moe_combine_bwd(const uint16_t* grad_out, const uint16_t* y, int64_t tokens, int64_t k,
+                          int64_t cols, const int32_t* rows, const int32_t* slots,
+                          const float* weights, uint16_t* grad_y, float* grad_weights,
+                          void* stream) {
+  MoeShape sh;
+  int st = moe_shape(tokens, k, cols, &sh), grid;
+  if (st) return st;
+  if (tokens == 0) return TRACE_OK;
+  if (!grad_out || !y || !rows || !slots || !weights || !grad_y || !grad_weights)
+    return TRACE_ERR_NULL;
+  if (!aligned(grad_out, 32) || !aligned(y, 32) || !aligned(rows, 4) || !aligned(slots, 4) ||
+      !aligned(weights, 4) || !aligned(grad_y, 32) || !aligned(grad_weights, 4))
+    return TRACE_ERR_ALIGN;
+  if ((st = moe_grid(sh.slots, &grid))) return st;
+  return launch(k_moe_combine_bwd, grid, (cudaStream_t)stream, (const V8*)grad_out, (const V8*)y,
+                sh, rows, slots, weights, (V8*)grad_y, grad_weights);
+}
+
+static int matmul_impl(bool mx, const uint8_t* a_codes, const uint8_t* a_scales,
+                       const float* a_gscale, int64_t rows, int64_t cols, int32_t num_groups,
+                       const int64_t* offs, int32_t a_layout, const uint8_t* w_codes,
+                       const uint8_t* w_scales, const float* w_gscale, int64_t n,
+                       int32_t num_matrices, int32_t w_layout, uint16_t* out, void* stream) {
+  int st = check_shape(rows, cols, num_groups, offs);
+  if (st) return st;
+  if (n < 1 || num_matrices < 1 || num_groups > TRACE_MATMUL_MAX_GROUPS ||
+      num_matrices > num_groups || !valid_layout(a_layout) || !valid_layout(w_layout) ||
+      rows > ((int64_t)1 << 31) - 512 || n * (long double)num_matrices > 2147483136.0L ||
+      cols > ((int64_t)1 << 31) - 512)
+    return TRACE_ERR_SHAPE;
+  if ((st = check_shape(n * num_matrices, cols, 1, nullptr))) return st;
+  if (rows == 0) return TRACE_OK;
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !out ||
+      (!mx && (!a_gscale || !w_gscale)))
+    return TRACE_ERR_NULL;
+  // tiled scales are read in 16-byte pieces
+  if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(out, 16) ||
+      (a_layout && !aligned(a_scales, 16)) || (w_layout && !aligned(w_scales, 16)) ||
+      !aligned(a_gscale, 4) || !aligned(w_gscale, 4) || !aligned(offs, 8))
+    return TRACE_ERR_ALIGN;
+  MmShape sh;
+  sh.rows = rows;
+  sh.n = n;
+  sh.cols = (uint32_t)cols;
+  sh.groups = num_groups;
+  sh.matrices = num_matrices;
+  sh.a_tiled = a_layout;
+  sh.w_tiled = w_layout;
+  int grid;
+  if ((st = moe_grid(((u64)rows * (u64)n + 31) / 32, &grid))) return st;
+  const int64_t* o = num_groups > 1 ? offs : nullptr;
+  return launch(mx ? k_matmul_simple<true> : k_matmul_simple<false>, grid, (cudaStream_t)stream,
+                a_codes, a_scales, a_gscale, o, w_codes, w_scales, w_gscale, sh, out);
+}
+
+int trace_fp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gscale,
+                     int64_t rows, int64_t cols, int32_t num_groups,
+                     const int64_t* group_row_offsets, int32_t a_scale_layout,
+                     const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gscale,
+                     int64_t n, int32_t num_matrices, int32_t w_scale_layout, uint16_t* out,
+                     void* stream) {
+  return matmul_impl(false, a_codes, a_scales, a_gscale, rows, cols, num_groups,
+                     group_row_offsets, a_scale_layout, w_codes, w_scales, w_gscale, n,
+                     num_matrices, w_scale_layout, out, stream);
+}
+
+int trace_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows, int64_t cols,
+                    int32_t num_groups, const int64_t* group_row_offsets, int32_t a_scale_layout,
+                    const uint8_t* w_codes, const uint8_t* w_scales, int64_t n,
+                    int32_t num_matrices, int32_t w_scale_layout, uint16_t* out, void* stream) {
+  return matmul_impl(true, a_codes, a_scales, nullptr, rows, cols, num_groups, group_row_offsets,
+                     a_scale_layout, w_codes, w_scales, nullptr, n, num_matrices, w_scale_layout,
+                     out, stream);
 }
 
 }  // extern "C"

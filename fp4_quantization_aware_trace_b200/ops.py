@@ -12,6 +12,7 @@ guided QAT fake-quant forward and its straight-through backward.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -114,6 +115,21 @@ def library() -> ctypes.CDLL:
         lib.trace_capture_amax_accumulate.restype = ctypes.c_int
         lib.trace_capture_with_amax.argtypes = [P, i64, i64, i32, P, P, P, P, P, P, i32, P]
         lib.trace_capture_with_amax.restype = ctypes.c_int
+        lib.trace_moe_sort_workspace_bytes.argtypes = [i64, i64, i32]
+        lib.trace_moe_sort_workspace_bytes.restype = sz
+        lib.trace_moe_sort.argtypes = [P, i32, i64, i64, i32, P, P, P, P, sz, P]
+        lib.trace_moe_sort.restype = ctypes.c_int
+        lib.trace_moe_dispatch.argtypes = [P, i64, i64, i64, P, P, P, P]
+        lib.trace_moe_dispatch.restype = ctypes.c_int
+        lib.trace_moe_combine.argtypes = [P, i64, i64, i64, P, P, P, P]
+        lib.trace_moe_combine.restype = ctypes.c_int
+        lib.trace_moe_combine_bwd.argtypes = [P, P, i64, i64, i64, P, P, P, P, P, P]
+        lib.trace_moe_combine_bwd.restype = ctypes.c_int
+        lib.trace_fp4_matmul.argtypes = [P, P, P, i64, i64, i32, P, i32, P, P, P, i64, i32, i32,
+                                         P, P]
+        lib.trace_fp4_matmul.restype = ctypes.c_int
+        lib.trace_mx_matmul.argtypes = [P, P, i64, i64, i32, P, i32, P, P, i64, i32, i32, P, P]
+        lib.trace_mx_matmul.restype = ctypes.c_int
         lib.trace_capture_status.argtypes = [P, P]
         lib.trace_capture_status.restype = ctypes.c_int
         _lib = lib
@@ -724,3 +740,294 @@ class GuidedFakeQuant(torch.autograd.Function):
     def backward(ctx, grad):
         (mask,) = ctx.saved_tensors
         return fq_bwd(grad.contiguous(), mask), None
+
+
+# ---------------------------------------------------------------------------
+# FP4 experts: the routing sort, tokens into expert order and back, and the
+# product of captured operands
+# ---------------------------------------------------------------------------
+
+@contextlib.contextmanager
+def _on(stream, *tensors):
+    """Work on the tensors' own device and on `stream` (default: that
+    device's current stream), so that outputs are allocated there too."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise TraceError(f"tensors on different devices: {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise TraceError("tensors passed to libtrace_fp4 must be CUDA tensors")
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch.cuda.current_stream(dev)
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+def _want(t: torch.Tensor, what: str, dtype, shape=None) -> None:
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TraceError(f"{what}: unexpected dtype {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise TraceError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def trace_moe_sort_workspace_bytes(tokens: int, k: int, num_experts: int) -> int:
+    return int(library().trace_moe_sort_workspace_bytes(tokens, k, num_experts))
+
+
+def trace_moe_sort(expert_ids, id_bytes, tokens, k, num_experts, offsets, rows, slots, workspace,
+                   workspace_bytes, stream=None) -> None:
+    _check(library().trace_moe_sort(_p(expert_ids), id_bytes, tokens, k, num_experts, _p(offsets),
+                                    _p(rows), _p(slots), _p(workspace), workspace_bytes,
+                                    _stream(stream)), "trace_moe_sort")
+
+
+def trace_moe_dispatch(x, tokens, k, cols, rows, slots, y, stream=None) -> None:
+    _check(library().trace_moe_dispatch(_p(x), tokens, k, cols, _p(rows), _p(slots), _p(y),
+                                        _stream(stream)), "trace_moe_dispatch")
+
+
+def trace_moe_combine(y, tokens, k, cols, rows, weights, out, stream=None) -> None:
+    _check(library().trace_moe_combine(_p(y), tokens, k, cols, _p(rows), _p(weights), _p(out),
+                                       _stream(stream)), "trace_moe_combine")
+
+
+def trace_moe_combine_bwd(grad_out, y, tokens, k, cols, rows, slots, weights, grad_y, grad_weights,
+                          stream=None) -> None:
+    _check(library().trace_moe_combine_bwd(_p(grad_out), _p(y), tokens, k, cols, _p(rows),
+                                           _p(slots), _p(weights), _p(grad_y), _p(grad_weights),
+                                           _stream(stream)), "trace_moe_combine_bwd")
+
+
+def trace_fp4_matmul(a_codes, a_scales, a_gscale, rows, cols, num_groups, offsets, a_scale_layout,
+                     w_codes, w_scales, w_gscale, n, num_matrices, w_scale_layout, out,
+                     stream=None) -> None:
+    _check(library().trace_fp4_matmul(_p(a_codes), _p(a_scales), _p(a_gscale), rows, cols,
+                                      num_groups, _p(offsets), a_scale_layout, _p(w_codes),
+                                      _p(w_scales), _p(w_gscale), n, num_matrices, w_scale_layout,
+                                      _p(out), _stream(stream)), "trace_fp4_matmul")
+
+
+def trace_mx_matmul(a_codes, a_scales, rows, cols, num_groups, offsets, a_scale_layout, w_codes,
+                    w_scales, n, num_matrices, w_scale_layout, out, stream=None) -> None:
+    _check(library().trace_mx_matmul(_p(a_codes), _p(a_scales), rows, cols, num_groups,
+                                     _p(offsets), a_scale_layout, _p(w_codes), _p(w_scales), n,
+                                     num_matrices, w_scale_layout, _p(out), _stream(stream)),
+           "trace_mx_matmul")
+
+
+@dataclasses.dataclass
+class MoeRoute:
+    """Where a batch's slots (token, choice) go: what moe_sort writes.
+    `offsets` groups the rows for capture: one group per expert and a last
+    one of the dropped slots (zero rows after dispatch)."""
+    offsets: torch.Tensor  # int64 [experts + 2]
+    rows: torch.Tensor     # int32 [tokens, k]: the slot's row, -1 if dropped
+    slots: torch.Tensor    # int32 [tokens * k]: the row's slot, -1 in the last group
+
+
+def moe_sort(expert_ids: torch.Tensor, num_experts: int, out: MoeRoute | None = None,
+             workspace: torch.Tensor | None = None, stream=None) -> MoeRoute:
+    """Stable sort of the slots of expert_ids (int32 / int64 [tokens, k]) by
+    expert; ids outside [0, num_experts) drop their slot."""
+    if expert_ids.dim() != 2 or expert_ids.shape[1] < 1:
+        raise TraceError("expert ids must be [tokens, k]")
+    _want(expert_ids, "expert ids", (torch.int32, torch.int64))
+    tokens, k = (int(v) for v in expert_ids.shape)
+    nbytes = trace_moe_sort_workspace_bytes(tokens, k, num_experts)
+    if nbytes == 0:
+        raise TraceError(f"moe_sort: {num_experts} experts for [{tokens}, {k}] ids")
+    dev = expert_ids.device
+    with _on(stream, expert_ids, workspace) as s:
+        if out is None:
+            out = MoeRoute(torch.empty(num_experts + 2, dtype=torch.int64, device=dev),
+                           torch.empty(tokens, k, dtype=torch.int32, device=dev),
+                           torch.empty(tokens * k, dtype=torch.int32, device=dev))
+        _want(out.offsets, "offsets", torch.int64, (num_experts + 2,))
+        _want(out.rows, "rows", torch.int32, (tokens, k))
+        _want(out.slots, "slots", torch.int32, (tokens * k,))
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        trace_moe_sort(expert_ids, expert_ids.element_size(), tokens, k, num_experts, out.offsets,
+                       out.rows, out.slots, workspace, workspace.numel() * workspace.element_size(),
+                       s)
+    return out
+
+
+def _route_of(route: MoeRoute) -> tuple[int, int]:
+    if route.rows.dim() != 2:
+        raise TraceError("route rows must be [tokens, k]")
+    tokens, k = (int(v) for v in route.rows.shape)
+    _want(route.rows, "route rows", torch.int32)
+    _want(route.slots, "route slots", torch.int32, (tokens * k,))
+    return tokens, k
+
+
+def moe_dispatch_fwd(x: torch.Tensor, route: MoeRoute, out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Tokens into expert order, bf16 [tokens, cols] -> [tokens * k, cols];
+    rows of the dropped group are zero."""
+    rows, cols = _bf16_2d(x)
+    tokens, k = _route_of(route)
+    _want(x, "tokens", torch.bfloat16, (tokens, cols))
+    with _on(stream, x, route.rows, route.slots, out) as s:
+        if out is None:
+            out = torch.empty(tokens * k, cols, dtype=torch.bfloat16, device=x.device)
+        _want(out, "out", torch.bfloat16, (tokens * k, cols))
+        trace_moe_dispatch(x, tokens, k, cols, route.rows, route.slots, out, s)
+    return out
+
+
+def moe_dispatch_bwd(grad: torch.Tensor, route: MoeRoute, out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Gradient of moe_dispatch_fwd: each token's rows summed in fp32."""
+    return moe_combine_fwd(grad, route, None, out, stream)
+
+
+def moe_combine_fwd(y: torch.Tensor, route: MoeRoute, weights: torch.Tensor | None,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Back to token order with the routing weights (float [tokens, k]; None:
+    all ones), bf16 [tokens * k, cols] -> [tokens, cols]."""
+    _, cols = _bf16_2d(y)
+    tokens, k = _route_of(route)
+    _want(y, "expert rows", torch.bfloat16, (tokens * k, cols))
+    if weights is not None:
+        _want(weights, "weights", torch.float32, (tokens, k))
+    with _on(stream, y, route.rows, weights, out) as s:
+        if out is None:
+            out = torch.empty(tokens, cols, dtype=torch.bfloat16, device=y.device)
+        _want(out, "out", torch.bfloat16, (tokens, cols))
+        trace_moe_combine(y, tokens, k, cols, route.rows, weights, out, s)
+    return out
+
+
+def moe_combine_bwd(grad: torch.Tensor, y: torch.Tensor, route: MoeRoute, weights: torch.Tensor,
+                    stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradients of moe_combine_fwd: (grad_y, grad_weights)."""
+    _, cols = _bf16_2d(y)
+    tokens, k = _route_of(route)
+    _want(y, "expert rows", torch.bfloat16, (tokens * k, cols))
+    _want(grad, "gradient", torch.bfloat16, (tokens, cols))
+    _want(weights, "weights", torch.float32, (tokens, k))
+    with _on(stream, grad, y, route.rows, route.slots, weights) as s:
+        grad_y = torch.empty_like(y)
+        grad_w = torch.empty(tokens, k, dtype=torch.float32, device=y.device)
+        trace_moe_combine_bwd(grad, y, tokens, k, cols, route.rows, route.slots, weights, grad_y,
+                              grad_w, s)
+    return grad_y, grad_w
+
+
+class MoeDispatch(torch.autograd.Function):
+    """Autograd wrapper of the dispatch; both directions run in the library."""
+
+    @staticmethod
+    def forward(ctx, x, route: MoeRoute):
+        ctx.save_for_backward(route.offsets, route.rows, route.slots)
+        return moe_dispatch_fwd(x, route)
+
+    @staticmethod
+    def backward(ctx, grad):
+        return moe_dispatch_bwd(grad.contiguous(), MoeRoute(*ctx.saved_tensors)), None
+
+
+class MoeCombine(torch.autograd.Function):
+    """Autograd wrapper of the combine (gradients to the rows and the weights)."""
+
+    @staticmethod
+    def forward(ctx, y, route: MoeRoute, weights):
+        ctx.save_for_backward(y, weights, route.offsets, route.rows, route.slots)
+        return moe_combine_fwd(y, route, weights)
+
+    @staticmethod
+    def backward(ctx, grad):
+        y, weights, *route = ctx.saved_tensors
+        grad_y, grad_w = moe_combine_bwd(grad.contiguous(), y, MoeRoute(*route), weights)
+        return grad_y, None, grad_w
+
+
+def moe_dispatch(x: torch.Tensor, route: MoeRoute) -> torch.Tensor:
+    """Differentiable dispatch of tokens into expert order (for
+    capture(y, route.offsets) and the grouped product)."""
+    if torch.is_grad_enabled() and x.requires_grad:
+        return MoeDispatch.apply(x, route)
+    return moe_dispatch_fwd(x, route)
+
+
+def moe_combine(y: torch.Tensor, route: MoeRoute, weights: torch.Tensor) -> torch.Tensor:
+    """Differentiable return to token order, weighted by the router."""
+    if torch.is_grad_enabled() and (y.requires_grad or weights.requires_grad):
+        return MoeCombine.apply(y, route, weights)
+    return moe_combine_fwd(y, route, weights)
+
+
+def _matmul_operand(cap, cols: int | None, what: str) -> tuple[int, int, int]:
+    """(rows, cols, scale layout) of a captured FP4 operand: row-major scales
+    are 2-D and tell cols; tiled ones are flat and need it."""
+    _want(cap.codes, f"{what} codes", torch.uint8)
+    _want(cap.scales, f"{what} scales", torch.uint8)
+    bs = 16 if isinstance(cap, Capture) else 32
+    layout = TRACE_SCALES_ROW_MAJOR if cap.scales.dim() == 2 else TRACE_SCALES_TILED_128x4
+    if cols is None:
+        if layout != TRACE_SCALES_ROW_MAJOR:
+            raise TraceError(f"{what}: cols is needed with tiled scales")
+        cols = int(cap.scales.shape[1]) * bs
+    if cols <= 0 or cols % 32 or cap.codes.numel() * 2 % cols:
+        raise TraceError(f"{what}: {cap.codes.numel()} bytes of codes are no rows of {cols}")
+    rows = cap.codes.numel() * 2 // cols
+    if cap.scales.numel() != trace_scale_bytes(rows, cols, bs, layout):
+        raise TraceError(f"{what}: {cap.scales.numel()} scales for [{rows}, {cols}]")
+    return rows, cols, layout
+
+
+def _matmul(a, w, cols, offsets, groups, matrices, out, stream, fmt):
+    rows, cols, la = _matmul_operand(a, cols, "a")
+    wrows, _, lw = _matmul_operand(w, cols, "w")
+    if matrices < 1 or wrows % matrices or wrows == 0:
+        raise TraceError(f"w: {wrows} rows are no {matrices} matrices")
+    n = wrows // matrices
+    with _on(stream, a.codes, a.scales, w.codes, w.scales, offsets, out) as s:
+        if out is None:
+            out = torch.empty(rows, n, dtype=torch.bfloat16, device=a.codes.device)
+        _want(out, "out", torch.bfloat16, (rows, n))
+        if fmt == "nvfp4":
+            _want(a.gscale, "a global scales", torch.float32, (groups,))
+            _want(w.gscale, "w global scales", torch.float32, (matrices,))
+            trace_fp4_matmul(a.codes, a.scales, a.gscale, rows, cols, groups, offsets, la, w.codes,
+                             w.scales, w.gscale, n, matrices, lw, out, s)
+        else:
+            trace_mx_matmul(a.codes, a.scales, rows, cols, groups, offsets, la, w.codes, w.scales,
+                            n, matrices, lw, out, s)
+    return out
+
+
+def fp4_matmul(a: Capture, w: Capture, cols: int | None = None, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Product of two NVFP4 captures, bf16 [rows, n]: a of [rows, cols], w of
+    one matrix [n, cols], or of one per expert stacked by rows (w.gscale has
+    one entry per matrix, a.offsets groups the rows).  Rows of a's groups
+    behind w's matrices (dropped slots) become zero.  cols is needed when
+    both scales are tiled.  Has no gradient: codes are the rollout's; the
+    training side differentiates through trace_fake_quant."""
+    if not isinstance(a, Capture) or not isinstance(w, Capture):
+        raise TraceError("fp4_matmul takes two NVFP4 captures")
+    if cols is None and a.scales.dim() != 2 and w.scales.dim() == 2:
+        cols = int(w.scales.shape[1]) * 16
+    rows = None if cols is None else a.codes.numel() * 2 // cols
+    return _matmul(a, w, cols, a.offsets, _groups(a.offsets, rows), int(w.gscale.numel()), out,
+                   stream, "nvfp4")
+
+
+def mx_matmul(a: MxCapture, w: MxCapture, cols: int | None = None,
+              offsets: torch.Tensor | None = None, groups: int = 1,
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Product of two MXFP4 captures, bf16 [rows, n]; grouped when `offsets`
+    (int64 row bounds of a) and `groups` (matrices stacked in w) are given."""
+    if not isinstance(a, MxCapture) or not isinstance(w, MxCapture):
+        raise TraceError("mx_matmul takes two MXFP4 captures")
+    if cols is None and a.scales.dim() != 2 and w.scales.dim() == 2:
+        cols = int(w.scales.shape[1]) * 32
+    rows = None if cols is None else a.codes.numel() * 2 // cols
+    return _matmul(a, w, cols, offsets, _groups(offsets, rows), groups, out, stream, "mxfp4")

@@ -466,6 +466,95 @@ int trace_capture_static_ws(const uint16_t* x, int64_t rows, int64_t cols,
                             uint32_t* mbits, uint8_t* scales, float* gscale,
                             void* stream);
 
+/* ---- FP4 experts ---------------------------------------------------------
+ * The rollout's own side of a captured site in a mixture-of-experts layer:
+ * the routing sort, tokens copied into expert order (the row groups that
+ * trace_capture takes) and back with the routing weights, each with its
+ * gradient, and the product of two captured operands.  The pages name the
+ * W4A4 GEMM and the MoE policy as the consumers of the codes and give no
+ * arithmetic for them; the definitions here are the usual ones.
+ *
+ * A slot is one (token, choice) pair, numbered token * k + choice; there are
+ * tokens * k < 2^31 of them.
+ *
+ * trace_moe_sort: a stable sort of the slots by expert.
+ *   expert_ids: int32 or int64 (id_bytes 4 or 8) [tokens, k]; an id outside
+ *             [0, num_experts) drops its slot (padding tokens, experts of
+ *             another rank).  The same expert may occur twice in a token.
+ *   offsets : out, int64[num_experts + 2]; expert e has the rows
+ *             [offsets[e], offsets[e+1]); the last group holds the dropped
+ *             slots, so offsets[num_experts + 1] == tokens * k and the array
+ *             is a valid group_row_offsets of num_experts + 1 groups.
+ *   rows    : out, int32 [tokens, k], the row of each slot; -1 if dropped.
+ *   slots   : out, int32 [tokens * k], the slot of each row; -1 in the last
+ *             group.  Rows of an expert are in slot order.
+ *   workspace: at least trace_moe_sort_workspace_bytes() bytes, 256-byte
+ *             aligned, contents of no account before and after; not shared
+ *             by calls that may run at the same time.
+ *   1 <= num_experts <= TRACE_MOE_MAX_EXPERTS, 1 <= k <= 65536. */
+#define TRACE_MOE_MAX_EXPERTS 4096
+size_t trace_moe_sort_workspace_bytes(int64_t tokens, int64_t k, int32_t num_experts);
+int trace_moe_sort(const void* expert_ids, int32_t id_bytes, int64_t tokens, int64_t k,
+                   int32_t num_experts, int64_t* offsets, int32_t* rows, int32_t* slots,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Tokens into expert order: y[rows[t, j]] = x[t] (bit copies); a row whose
+ * `slots` entry is negative becomes +0.  x: bf16 [tokens, cols]; y: bf16
+ * [tokens * k, cols]; both 32-byte aligned, cols a multiple of 32; rows and
+ * slots as trace_moe_sort writes them (an entry outside its range is
+ * skipped).  y must not overlap x.  The gradient, dx[t] = sum_j
+ * dy[rows[t, j]], is trace_moe_combine(dy, ..., weights = NULL, dx). */
+int trace_moe_dispatch(const uint16_t* x, int64_t tokens, int64_t k, int64_t cols,
+                       const int32_t* rows, const int32_t* slots, uint16_t* y, void* stream);
+
+/* Back to token order: out[t] = bf16(sum over j of weights[t, j] *
+ * y[rows[t, j]]), accumulated in fp32 by one FMA per term in the order of j;
+ * dropped slots add nothing whatever their weight.  y: bf16
+ * [tokens * k, cols]; weights: float [tokens, k] or NULL for all ones; out:
+ * bf16 [tokens, cols].  y and out 32-byte aligned, not overlapping. */
+int trace_moe_combine(const uint16_t* y, int64_t tokens, int64_t k, int64_t cols,
+                      const int32_t* rows, const float* weights, uint16_t* out, void* stream);
+
+/* Gradients of trace_moe_combine: grad_y[rows[t, j]] = bf16(weights[t, j] *
+ * grad_out[t]) (+0 in rows without a slot) and grad_weights[t, j] =
+ * sum over columns of grad_out[t] * y[rows[t, j]] in fp32 (0 for a dropped
+ * slot).  Shapes and alignment as above; grad_weights: float [tokens, k].
+ * No output overlaps an input. */
+int trace_moe_combine_bwd(const uint16_t* grad_out, const uint16_t* y, int64_t tokens, int64_t k,
+                          int64_t cols, const int32_t* rows, const int32_t* slots,
+                          const float* weights, uint16_t* grad_y, float* grad_weights,
+                          void* stream);
+
+/* Product of two captured operands, dense or grouped:
+ *   out[r, j] = bf16(a_gscale[g] * w_gscale[g] * sum over k of
+ *               (code * block scale of a at r, k) *
+ *               (code * block scale of w at g * n + j, k)),
+ * g the group of row r (trace_mx_matmul: E8M0 scales and no global scales).
+ * The terms are exact and the sum is held in fp32.
+ *   a_*     : a capture of [rows, cols] with num_groups groups (offsets as
+ *             everywhere; NULL for one group).
+ *   w_*     : a capture of num_matrices matrices [n, cols] stacked by rows,
+ *             w_gscale float[num_matrices].  num_matrices <= num_groups <=
+ *             TRACE_MATMUL_MAX_GROUPS; rows of the groups from num_matrices
+ *             on (the dropped slots of trace_moe_sort) become +0, and rows
+ *             from offsets[num_groups] on are left as they were.
+ *   layouts : TRACE_SCALES_*, one for each operand.  The padding of a tiled
+ *             array is not used, whatever it holds.
+ *   out     : bf16 [rows, n], 16-byte aligned; must not overlap an input.
+ *   codes 16-byte aligned, tiled scales 16-byte aligned; n >= 1 (no multiple
+ *   needed); rows, cols and n * num_matrices below 2^31 - 512. */
+#define TRACE_MATMUL_MAX_GROUPS 4097
+int trace_fp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gscale,
+                     int64_t rows, int64_t cols, int32_t num_groups,
+                     const int64_t* group_row_offsets, int32_t a_scale_layout,
+                     const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gscale,
+                     int64_t n, int32_t num_matrices, int32_t w_scale_layout, uint16_t* out,
+                     void* stream);
+int trace_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows, int64_t cols,
+                    int32_t num_groups, const int64_t* group_row_offsets, int32_t a_scale_layout,
+                    const uint8_t* w_codes, const uint8_t* w_scales, int64_t n,
+                    int32_t num_matrices, int32_t w_scale_layout, uint16_t* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,107 @@
+"""Refusals of the FP4 expert operators, before any CUDA call (no GPU), and
+the size queries."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+from fp4_quantization_aware_trace_b200 import _build, ops
+
+P = ctypes.c_void_p
+A = P(1 << 20)            # aligned fake pointers: never dereferenced
+ODD = P((1 << 20) + 2)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return ops.library()
+
+
+def test_sort_workspace_query(lib):
+    f = ops.trace_moe_sort_workspace_bytes
+    assert f(0, 8, 128) == 256 and f(512, 8, 128) == 256
+    assert f(513, 8, 128) == -(-2 * 129 * 4 // 256) * 256
+    for bad in [(-1, 8, 4), (4, 0, 4), (4, 8, 0), (4, 8, 4097), (1 << 31, 1, 4), (1 << 30, 2, 4),
+                (4, 65537, 4)]:
+        assert f(*bad) == 0
+
+
+def test_sort_refusals(lib):
+    f = lib.trace_moe_sort
+    assert f(A, 4, -1, 8, 4, A, A, A, A, 256, None) == 2
+    assert f(A, 4, 4, 0, 4, A, A, A, A, 256, None) == 2
+    assert f(A, 2, 4, 8, 4, A, A, A, A, 256, None) == 2
+    assert f(A, 4, 4, 8, 4097, A, A, A, A, 256, None) == 2
+    assert f(A, 4, 1 << 30, 2, 4, A, A, A, A, 256, None) == 2
+    assert f(None, 4, 4, 8, 4, A, A, A, A, 256, None) == 1
+    assert f(A, 4, 4, 8, 4, A, A, A, None, 256, None) == 1
+    assert f(P((1 << 20) + 4), 8, 4, 8, 4, A, A, A, A, 256, None) == 3
+    assert f(A, 4, 4, 8, 4, P((1 << 20) + 4), A, A, A, 256, None) == 3
+    assert f(A, 4, 4, 8, 4, A, A, A, A, 255, None) == 4
+
+
+def test_token_refusals(lib):
+    d, c, b = lib.trace_moe_dispatch, lib.trace_moe_combine, lib.trace_moe_combine_bwd
+    assert d(A, 4, 2, 48, A, A, A, None) == 2 and c(A, 4, 2, 0, A, A, A, None) == 2
+    assert d(A, -1, 2, 32, A, A, A, None) == 2 and b(A, A, 1 << 31, 1, 32, A, A, A, A, A, None) == 2
+    assert d(None, 4, 2, 32, A, A, A, None) == 1 and c(A, 4, 2, 32, None, A, A, None) == 1
+    assert b(A, A, 4, 2, 32, A, A, None, A, A, None) == 1
+    assert d(P((1 << 20) + 16), 4, 2, 32, A, A, A, None) == 3
+    assert c(A, 4, 2, 32, A, ODD, A, None) == 3
+    assert b(A, A, 4, 2, 32, A, A, A, P((1 << 20) + 16), A, None) == 3
+    assert d(None, 0, 2, 32, None, None, None, None) == 0
+
+
+def test_product_refusals(lib):
+    def nv(rows=4, cols=64, groups=1, offs=None, la=0, n=8, mats=1, lw=0, a=A, out=A, ws=A, ag=A):
+        return lib.trace_fp4_matmul(a, A, ag, rows, cols, groups, offs, la, A, ws, A, n, mats, lw,
+                                    out, None)
+
+    def mx(rows=4, cols=64, groups=1, offs=None, la=0, n=8, mats=1, lw=0, a=A, out=A):
+        return lib.trace_mx_matmul(a, A, rows, cols, groups, offs, la, A, A, n, mats, lw, out, None)
+
+    for f in (nv, mx):
+        assert f(cols=48) == 2 and f(cols=0) == 2 and f(rows=-1) == 2 and f(n=0) == 2
+        assert f(la=2) == 2 and f(lw=-1) == 2 and f(mats=0) == 2
+        assert f(groups=2, offs=A, mats=3) == 2 and f(groups=4098, offs=A) == 2
+        assert f(rows=(1 << 31) - 511) == 2 and f(n=1 << 31) == 2
+        assert f(groups=4000, offs=A, n=1 << 20, mats=4000) == 2
+        assert f(groups=2) == 1 and f(a=None) == 1 and f(out=None) == 1
+        assert f(a=P((1 << 20) + 8)) == 3 and f(out=P((1 << 20) + 8)) == 3
+        assert f(groups=2, offs=P((1 << 20) + 4)) == 3
+        assert f(rows=0, a=None, out=None) == 0
+    assert nv(ag=None) == 1
+    assert nv(lw=1, ws=P((1 << 20) + 8)) == 3
+
+
+def test_binding_refusals(lib):
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    f32 = torch.ones(1)
+    a = ops.Capture(u8(4 * 32), None, u8(4, 4), f32)
+    m = ops.MxCapture(u8(4 * 32), None, u8(4, 2))
+    flat = ops.Capture(u8(4 * 32), None, u8(512), f32)
+    for call in (lambda: ops.fp4_matmul(a, a),                        # host tensors
+                 lambda: ops.fp4_matmul(flat, flat),                  # cols unknown
+                 lambda: ops.fp4_matmul(a, a, 48),
+                 lambda: ops.fp4_matmul(a, a, 32),                    # scales of another shape
+                 lambda: ops.fp4_matmul(a, m),
+                 lambda: ops.mx_matmul(m, a),
+                 lambda: ops.mx_matmul(m, m, groups=3),
+                 lambda: ops.mx_matmul(ops.MxCapture(u8(4 * 64), None, u8(4, 2)), m),  # E4M3 codes
+                 lambda: ops.moe_sort(torch.zeros(3, dtype=torch.int32), 4),
+                 lambda: ops.moe_sort(torch.zeros(3, 2), 4),
+                 lambda: ops.moe_sort(torch.zeros(3, 2, dtype=torch.int32), 4),
+                 lambda: ops.moe_sort(torch.zeros(3, 2, dtype=torch.int32), 0)):
+        with pytest.raises(ops.TraceError):
+            call()
+    route = ops.MoeRoute(torch.zeros(6, dtype=torch.int64), torch.zeros(3, 2, dtype=torch.int32),
+                         torch.zeros(6, dtype=torch.int32))
+    x, y, w = torch.zeros(3, 32).bfloat16(), torch.zeros(6, 32).bfloat16(), torch.zeros(3, 2)
+    for call in (lambda: ops.moe_dispatch(x, route), lambda: ops.moe_dispatch(y, route),
+                 lambda: ops.moe_dispatch(x.float(), route), lambda: ops.moe_combine(x, route, w),
+                 lambda: ops.moe_combine(y, route, w.double()), lambda: ops.moe_combine(y, route, w)):
+        with pytest.raises(ops.TraceError):
+            call()

@@ -1,0 +1,470 @@
+"""The FP4 expert operators on the GPU against plain 64-bit forms: routing
+sort, dispatch, combine with their gradients, the product of captured
+operands, and a whole expert layer of them."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import _experts as ref
+from fp4_quantization_aware_trace_b200 import inputs, ops
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _gen(seed):
+    g = torch.Generator(device="cpu")
+    g.manual_seed(seed)
+    return g
+
+
+# ---------------------------------------------------------------------------
+# Sort
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("tokens,k,experts", [
+    (1, 1, 1), (1, 8, 128), (3, 2, 5), (37, 8, 128), (511, 8, 128), (512, 8, 128), (513, 8, 128),
+    (4096, 1, 4096), (4099, 3, 7), (1000, 5, 4096), (20001, 8, 300)])
+def test_sort(tokens, k, experts, dtype):
+    g = _gen(tokens * 31 + k + experts)
+    ids = torch.randint(-1, experts + 1, (tokens, k), generator=g).to(dtype)  # both ends are dropped
+    if dtype == torch.int64 and tokens > 2:
+        ids[1, 0] = (1 << 40) + min(3, experts - 1)  # in range only in its low word
+        ids[2, 0] = -(1 << 40) + min(3, experts - 1)
+    route = ops.moe_sort(ids.to(DEV), experts)
+    offsets, rows, slots = ref.sort(ids.numpy(), experts)
+    assert np.array_equal(route.offsets.cpu().numpy(), offsets)
+    assert np.array_equal(route.rows.cpu().numpy(), rows)
+    assert np.array_equal(route.slots.cpu().numpy(), slots)
+    assert ops.validate_offsets(route.offsets, tokens * k) == 0
+
+
+@pytest.mark.parametrize("fill", [-1, 0, 6])
+def test_sort_one_value(fill):
+    """Every slot dropped; every slot to the first or the last expert."""
+    ids = torch.full((2500, 4), fill, dtype=torch.int32)
+    route = ops.moe_sort(ids.to(DEV), 7)
+    for got, want in zip((route.offsets, route.rows, route.slots), ref.sort(ids.numpy(), 7)):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
+def test_sort_no_tokens():
+    route = ops.moe_sort(torch.empty(0, 8, dtype=torch.int64, device=DEV), 16)
+    assert route.offsets.tolist() == [0] * 18 and route.rows.shape == (0, 8)
+
+
+def test_sort_reuses_a_dirty_workspace_and_outputs():
+    ids = torch.randint(0, 40, (3000, 8), generator=_gen(5), dtype=torch.int32)
+    ws = torch.full((ops.trace_moe_sort_workspace_bytes(3000, 8, 40),), 0xA5, dtype=torch.uint8,
+                    device=DEV)
+    route = None
+    for seed in (1, 2):
+        ids = torch.randint(0, 40, (3000, 8), generator=_gen(seed), dtype=torch.int32)
+        route = ops.moe_sort(ids.to(DEV), 40, out=route, workspace=ws)
+        for got, want in zip((route.offsets, route.rows, route.slots), ref.sort(ids.numpy(), 40)):
+            assert np.array_equal(got.cpu().numpy(), want)
+
+
+# ---------------------------------------------------------------------------
+# Dispatch and combine
+# ---------------------------------------------------------------------------
+
+def _route(tokens, k, experts, seed, dropped=0.2):
+    g = _gen(seed)
+    ids = torch.randint(0, experts, (tokens, k), generator=g)
+    ids[torch.rand(tokens, k, generator=g) < dropped] = -1
+    return ops.moe_sort(ids.to(DEV), experts), ref.sort(ids.numpy(), experts)
+
+
+TOKEN_CASES = [(1, 1, 32, 1), (1, 8, 2048, 128), (7, 3, 96, 4), (33, 8, 544, 16), (130, 1, 512, 8),
+               (257, 9, 1056, 64)]
+
+
+@pytest.mark.parametrize("tokens,k,cols,experts", TOKEN_CASES)
+def test_dispatch_and_its_gradient(tokens, k, cols, experts):
+    route, (offsets, rows, slots) = _route(tokens, k, experts, 11 * tokens + k)
+    g = _gen(tokens)
+    x = torch.randn(tokens, cols, generator=g).to(torch.bfloat16)
+    dy = torch.randn(tokens * k, cols, generator=g).to(torch.bfloat16)
+    xg = x.to(DEV).requires_grad_()
+    y = ops.moe_dispatch(xg, route)
+    want = np.zeros((tokens * k, cols))
+    live = slots >= 0
+    want[live] = ref.f64(x)[slots[live] // k]
+    assert np.array_equal(ref.f64(y), want)
+    (dx,) = torch.autograd.grad(y, xg, dy.to(DEV))
+    d = ref.f64(dy)
+    parts = np.where((rows >= 0)[..., None], d[np.maximum(rows, 0)], 0.0)
+    exact, mag = parts.sum(1), np.abs(parts).sum(1)
+    # k additions in fp32 and one rounding to bf16
+    err = np.abs(ref.f64(dx) - exact)
+    assert np.all(err <= 2.0 ** -8 * np.abs(exact) + (1 + 2.0 ** -8) * k * 2.0 ** -24 * mag)
+
+
+@pytest.mark.parametrize("tokens,k,cols,experts", TOKEN_CASES)
+def test_combine_and_its_gradients(tokens, k, cols, experts):
+    route, (offsets, rows, slots) = _route(tokens, k, experts, 13 * tokens + k)
+    g = _gen(tokens + 1)
+    y = torch.randn(tokens * k, cols, generator=g).to(torch.bfloat16)
+    w = torch.softmax(torch.randn(tokens, k, generator=g), 1)
+    do = torch.randn(tokens, cols, generator=g).to(torch.bfloat16)
+    # what dropped slots hold must not matter
+    yb, wb = y.clone(), w.clone()
+    yb[torch.from_numpy(slots < 0)] = float("nan")
+    wb[torch.from_numpy(rows < 0)] = float("inf")
+    yg, wg = yb.to(DEV).requires_grad_(), wb.to(DEV).requires_grad_()
+    out = ops.moe_combine(yg, route, wg)
+    dyg, dwg = torch.autograd.grad(out, (yg, wg), do.to(DEV))
+    live = rows >= 0
+    yr = np.where(live[..., None], ref.f64(y)[np.maximum(rows, 0)], 0.0)
+    terms = yr * ref.f64(w)[..., None]
+    exact, mag = terms.sum(1), np.abs(terms).sum(1)
+    err = np.abs(ref.f64(out) - exact)
+    # k fused multiply-adds in fp32 and one rounding to bf16
+    assert np.all(err <= 2.0 ** -8 * np.abs(exact) + (1 + 2.0 ** -8) * k * 2.0 ** -24 * mag)
+    # dweights: products exact in fp32 (8 x 8 bits), at most cols + 5 additions
+    dots = ref.f64(do)[:, None, :] * yr
+    dw, dmag = dots.sum(-1), np.abs(dots).sum(-1)
+    assert np.all(np.abs(ref.f64(dwg) - dw) <= (cols + 5) * 2.0 ** -24 * dmag)
+    # grad_y: one product in fp32, one rounding to bf16
+    dy = np.zeros((tokens * k, cols))
+    s = slots[slots >= 0]
+    dy[slots >= 0] = ref.f64(do)[s // k] * ref.f64(w).reshape(-1)[s][:, None]
+    assert np.all(np.abs(ref.f64(dyg) - dy) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(dy) + 2.0 ** -134)
+
+
+def test_gradients_against_differences():
+    """Small whole numbers, so that every sum is exact and a difference
+    quotient of the (linear) forward is the gradient."""
+    tokens, k, cols, experts = 5, 3, 64, 4
+    route, _ = _route(tokens, k, experts, 3)
+    g = _gen(4)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g).float().to(DEV)  # noqa: E731
+    x, y = ints(tokens, cols).bfloat16(), ints(tokens * k, cols).bfloat16()
+    w, do, dyy = ints(tokens, k), ints(tokens, cols).bfloat16(), ints(tokens * k, cols).bfloat16()
+    xg = x.clone().requires_grad_()
+    (dx,) = torch.autograd.grad(ops.moe_dispatch(xg, route), xg, dyy)
+    yg, wg = y.clone().requires_grad_(), w.clone().requires_grad_()
+    dy, dw = torch.autograd.grad(ops.moe_combine(yg, route, wg), (yg, wg), do)
+
+    def slope(f, v, grad_out, at):
+        hi = v.clone()
+        hi.view(-1)[at] += 1
+        return ((f(hi).double() - f(v).double()) * grad_out.double()).sum().item()
+
+    for at in (0, 17, tokens * cols - 1):
+        assert slope(lambda v: ops.moe_dispatch(v, route), x, dyy, at) == dx.view(-1)[at].item()
+    for at in (0, 129, tokens * k * cols - 1):
+        assert slope(lambda v: ops.moe_combine(v, route, w), y, do, at) == dy.view(-1)[at].item()
+    for at in range(tokens * k):
+        assert slope(lambda v: ops.moe_combine(y, route, v), w, do, at) == dw.view(-1)[at].item()
+
+
+def test_gradients_of_views_and_shared_leaves():
+    """An expanded (stride 0) upstream gradient; the same tokens dispatched twice."""
+    route, (_, rows, _) = _route(9, 2, 4, 21)
+    x = torch.ones(9, 64, dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    a, b = ops.moe_dispatch(x, route), ops.moe_dispatch(x, route)
+    (a.sum() + 2 * b.sum()).backward()
+    want = 3.0 * (rows >= 0).sum(1)
+    assert np.array_equal(ref.f64(x.grad), np.repeat(want[:, None], 64, 1))
+
+
+def test_bad_route_entries_are_skipped():
+    """Entries outside the rows: no access, no term."""
+    route, _ = _route(6, 2, 3, 8, dropped=0.0)
+    y = torch.ones(12, 64, dtype=torch.bfloat16, device=DEV)
+    rows = route.rows.clone()
+    rows[2, 0], rows[3, 1] = 12, 2 ** 31 - 1
+    bad = ops.MoeRoute(route.offsets, rows, route.slots)
+    out = ops.moe_combine(y, bad, torch.ones(6, 2, device=DEV))
+    assert out[:, 0].tolist() == [2, 2, 1, 1, 2, 2]
+
+
+# ---------------------------------------------------------------------------
+# Product
+# ---------------------------------------------------------------------------
+
+def _capture(x, fmt, tiled, offsets=None):
+    if fmt == "nvfp4":
+        return ops.capture_tiled(x, offsets) if tiled else ops.capture(x, offsets)
+    return ops.mx_capture_tiled(x) if tiled else ops.mx_capture(x)
+
+
+def _operand(cap, rows, cols, fmt):
+    scols = cols // (16 if fmt == "nvfp4" else 32)
+    s = cap.scales.cpu().numpy()
+    s = s if s.ndim == 2 else ref.untile(s, rows, scols)
+    return ref.operand(cap.codes.cpu().numpy(), s, rows, cols, fmt)
+
+
+def _poison(cap, rows, cols, fmt):
+    """NaN bytes in the padding of a tiled scale array."""
+    scols = cols // (16 if fmt == "nvfp4" else 32)
+    s = ref.untile(cap.scales.cpu().numpy(), rows, scols)
+    cap.scales = torch.from_numpy(ref.tile(s, 0xFF)).to(DEV)
+
+
+def _matmul(a, w, cols, fmt, offsets, groups, out=None, stream=None):
+    if fmt == "nvfp4":
+        return ops.fp4_matmul(a, w, cols, out=out, stream=stream)
+    return ops.mx_matmul(a, w, cols, offsets=offsets, groups=groups, out=out, stream=stream)
+
+
+def _product_case(rows, n, cols, fmt, tiled_a, tiled_w, counts=None, seed=0):
+    """counts: rows of each group; the last one of a `None`-terminated list
+    has no matrix."""
+    matrices = 1
+    offs = None
+    if counts is not None:
+        matrices = len(counts) - (1 if counts[-1] is None else 0)
+        known = [c for c in counts if c is not None]
+        bounds = np.concatenate([[0], np.cumsum(known)])
+        if counts[-1] is None:
+            bounds = np.concatenate([bounds, [rows]])
+        assert bounds[-1] == rows
+        offs = torch.from_numpy(bounds.astype(np.int64)).to(DEV)
+    a = inputs.tiny_site(seed + 1, rows, cols).x_roll.to(DEV)
+    w = (0.05 * inputs.tiny_site(seed + 2, matrices * n, cols).x_roll.float()).bfloat16().to(DEV)
+    wo = torch.arange(matrices + 1, dtype=torch.int64, device=DEV) * n if matrices > 1 else None
+    ca, cw = _capture(a, fmt, tiled_a, offs), _capture(w, fmt, tiled_w, wo)
+    for cap, r, t in ((ca, rows, tiled_a), (cw, matrices * n, tiled_w)):
+        if t:
+            _poison(cap, r, cols, fmt)
+    pad = 4096
+    buf = torch.full((rows * n + 2 * pad,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[pad:pad + rows * n].view(rows, n)
+    _matmul(ca, cw, cols, fmt, offs, matrices, out=out)
+    ga = ca.gscale.cpu().numpy() if fmt == "nvfp4" else None
+    gw = cw.gscale.cpu().numpy() if fmt == "nvfp4" else None
+    bounds = [0, rows] if offs is None else offs.tolist()
+    exact, mag = ref.product(_operand(ca, rows, cols, fmt), _operand(cw, matrices * n, cols, fmt),
+                             ga, gw, bounds, n)
+    err = np.abs(ref.f64(out) - exact)
+    bound = ref.product_bound(exact, mag, cols)
+    assert np.all(err <= bound), (int(np.sum(~(err <= bound))), np.argwhere(~(err <= bound))[:4],
+                                  float(np.nanmax(err - bound)))
+    edge = torch.cat([buf[:pad], buf[pad + rows * n:]])
+    assert bool((edge == 7.0).all())
+
+
+FORMATS = ["nvfp4", "mxfp4"]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,n,cols", [
+    (1, 1, 32), (1, 128, 64), (1, 4096, 2048), (2, 130, 96), (3, 8, 4096), (16, 256, 256),
+    (17, 129, 160), (29, 2048, 1024), (33, 40, 288), (64, 384, 512), (65, 127, 544),
+    (128, 128, 128), (129, 257, 320), (200, 1000, 768), (256, 512, 2048), (300, 264, 1056),
+    (1000, 640, 224), (2049, 136, 1024)])
+def test_product(fmt, rows, n, cols):
+    _product_case(rows, n, cols, fmt, rows % 2 == 0, n % 2 == 0, seed=rows + n)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tiled_a", [False, True])
+@pytest.mark.parametrize("tiled_w", [False, True])
+def test_product_layouts(fmt, tiled_a, tiled_w):
+    for cols in (352, 512):
+        _product_case(150, 200, cols, fmt, tiled_a, tiled_w, seed=cols)
+
+
+GROUPS = [
+    [5], [0, 7], [7, 0], [1] * 9, [3, 0, 0, 130, 1, 64], [128, 128, 256], [127, 129, 0, 1, 255],
+    [300, 2, 17], [4, 9, None], [0, 0, None], [40, None], [16] * 24]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("counts", GROUPS, ids=str)
+@pytest.mark.parametrize("n,cols,tiled", [(136, 288, True), (128, 512, True), (72, 96, False)])
+def test_grouped_product(fmt, counts, n, cols, tiled):
+    rows = sum(c for c in counts if c is not None) + (21 if counts[-1] is None else 0)
+    _product_case(rows, n, cols, fmt, tiled, tiled, counts, seed=len(counts) + rows)
+
+
+def test_grouped_product_many_groups():
+    g = _gen(77)
+    counts = torch.randint(0, 6, (1024,), generator=g).tolist()
+    counts[500] = 300
+    _product_case(sum(counts), 40, 64, "nvfp4", True, True, counts, seed=9)
+
+
+def test_product_rows_behind_the_last_group_are_left():
+    rows, n, cols = 70, 96, 128
+    a = inputs.tiny_site(1, rows, cols).x_roll.to(DEV)
+    w = inputs.tiny_site(2, 2 * n, cols).x_roll.to(DEV)
+    offs = torch.tensor([0, 30, 70], dtype=torch.int64, device=DEV)
+    ca = ops.capture(a, offs)
+    cw = ops.capture(w, torch.tensor([0, n, 2 * n], dtype=torch.int64, device=DEV))
+    whole = ops.fp4_matmul(ca, cw)
+    out = torch.full((rows, n), 5.0, dtype=torch.bfloat16, device=DEV)
+    ca.offsets = torch.tensor([0, 30, 41], dtype=torch.int64, device=DEV)
+    ops.fp4_matmul(ca, cw, out=out)
+    assert torch.equal(out[:41], whole[:41]) and bool((out[41:] == 5.0).all())
+
+
+@pytest.mark.parametrize("ga,gw", [(1e-38, 1e30), (3e35, 1e-36), (1e-20, 1e-20), (1e30, 1e30),
+                                   (2.0 ** -140, 2.0 ** 100)])
+def test_product_extreme_global_scales(ga, gw):
+    """The product of the scales may leave fp32's range where the output does not."""
+    rows, n, cols = 20, 24, 64
+    g = _gen(3)
+    codes = lambda r: torch.randint(0, 256, (r * cols // 2,), generator=g, dtype=torch.uint8)  # noqa: E731
+    ac, wc = codes(rows).to(DEV), codes(n).to(DEV)
+    s = torch.randint(0x20, 0x50, (rows + n, cols // 16), generator=g, dtype=torch.uint8).to(DEV)
+    a = ops.Capture(ac, None, s[:rows].contiguous(), torch.tensor([ga], device=DEV))
+    w = ops.Capture(wc, None, s[rows:].contiguous(), torch.tensor([gw], device=DEV))
+    out = ref.f64(ops.fp4_matmul(a, w))
+    exact, mag = ref.product(_operand(a, rows, cols, "nvfp4"), _operand(w, n, cols, "nvfp4"),
+                             a.gscale.cpu().numpy(), w.gscale.cpu().numpy(), [0, rows], n)
+    over = np.abs(exact) > 3.3e38
+    inside = np.abs(exact) < 3.3e38
+    bound = ref.product_bound(exact, mag, cols)
+    assert np.all(np.isinf(out[over]))
+    assert np.all(np.abs(out - exact)[inside] <= bound[inside])
+
+
+def test_product_of_the_largest_and_of_zero_codes():
+    """Every term at its largest (6 * 448 each side), and operands of zeros."""
+    rows, n, cols = 5, 136, 4096
+    full = lambda r: torch.full((r * cols // 2,), 0x77, dtype=torch.uint8, device=DEV)  # noqa: E731
+    top = lambda r: torch.full((r, cols // 16), 0x7E, dtype=torch.uint8, device=DEV)  # noqa: E731
+    one = torch.ones(1, device=DEV)
+    a = ops.Capture(full(rows), None, top(rows), one)
+    w = ops.Capture(full(n), None, top(n), one)
+    want = torch.tensor(float(cols * 2688 ** 2)).bfloat16().item()
+    assert bool((ops.fp4_matmul(a, w) == want).all())
+    a.scales = torch.zeros_like(a.scales)
+    assert bool((ops.fp4_matmul(a, w) == 0).all())
+    z = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    assert bool((ops.fp4_matmul(ops.capture(z), w) == 0).all())
+    assert bool((ops.mx_matmul(ops.mx_capture(z), ops.mx_capture(z)) == 0).all())
+
+
+def test_product_no_rows():
+    a = ops.Capture(torch.empty(0, dtype=torch.uint8, device=DEV), None,
+                    torch.empty(0, 4, dtype=torch.uint8, device=DEV), torch.ones(1, device=DEV))
+    w = ops.capture(inputs.tiny_site(2, 40, 64).x_roll.to(DEV))
+    assert ops.fp4_matmul(a, w).shape == (0, 40)
+
+
+def test_product_repeats_bit_for_bit_and_on_two_streams():
+    rows, n, cols = 40, 1024, 4096
+    a = ops.capture_tiled(inputs.tiny_site(1, rows, cols).x_roll.to(DEV))
+    w = ops.capture_tiled(inputs.tiny_site(2, n, cols).x_roll.to(DEV))
+    first = ops.fp4_matmul(a, w, cols)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [ops.fp4_matmul(a, w, cols, stream=s) for _ in range(8) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, o) for o in outs)
+
+
+# ---------------------------------------------------------------------------
+# Together
+# ---------------------------------------------------------------------------
+
+def _layer(x, ids, weights, w, experts, n, cols):
+    route = ops.moe_sort(ids, experts)
+    xs = ops.moe_dispatch(x, route)
+    a = ops.capture_tiled(xs, route.offsets)
+    y = ops.fp4_matmul(a, w, cols)
+    return ops.moe_combine(y, route, weights), route, a, y
+
+
+@pytest.mark.parametrize("tokens", [1, 45, 300])
+def test_expert_layer(tokens):
+    """Sort, dispatch, capture, grouped product, combine, as a rollout runs
+    them, against 64 bits from capture's codes; then captured into a graph
+    and replayed on other inputs."""
+    k, experts, n, cols = 4, 12, 160, 256
+    g = _gen(tokens)
+    ids = torch.stack([torch.randperm(experts, generator=g)[:k] for _ in range(tokens)]).int()
+    if tokens > 8:
+        ids[5:9] = -1
+    x = torch.randn(tokens, cols, generator=g).bfloat16()
+    weights = torch.softmax(torch.randn(tokens, k, generator=g), 1)
+    wt = (0.1 * torch.randn(experts * n, cols, generator=g)).bfloat16().to(DEV)
+    w = ops.capture_tiled(wt, torch.arange(experts + 1, dtype=torch.int64, device=DEV) * n)
+    args = [v.to(DEV) for v in (x, ids, weights)]
+    out, route, a, y = _layer(*args, w, experts, n, cols)
+
+    def check(out, route, a, y, weights):
+        bounds = route.offsets.tolist()
+        exact, mag = ref.product(_operand(a, tokens * k, cols, "nvfp4"),
+                                 _operand(w, experts * n, cols, "nvfp4"), a.gscale.cpu().numpy(),
+                                 w.gscale.cpu().numpy(), bounds, n)
+        assert np.all(np.abs(ref.f64(y) - exact) <= ref.product_bound(exact, mag, cols))
+        rows = route.rows.cpu().numpy()
+        terms = np.where((rows >= 0)[..., None], ref.f64(y)[np.maximum(rows, 0)], 0.0) \
+            * ref.f64(weights)[..., None]
+        s, m = terms.sum(1), np.abs(terms).sum(1)
+        assert np.all(np.abs(ref.f64(out) - s) <= 2.0 ** -8 * np.abs(s)
+                      + (1 + 2.0 ** -8) * k * 2.0 ** -24 * m)
+
+    check(out, route, a, y, weights)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        _layer(*args, w, experts, n, cols)
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            held = _layer(*args, w, experts, n, cols)
+    torch.cuda.synchronize()
+    for seed in (1, 2):
+        g = _gen(100 + seed)
+        args[0].copy_(torch.randn(tokens, cols, generator=g).bfloat16())
+        args[1].copy_(torch.randint(0, experts, (tokens, k), generator=g).int())
+        graph.replay()
+        torch.cuda.synchronize()
+        check(*held, weights)
+
+
+def test_training_layer_gradients():
+    """Dispatch, guided fake-quant against the rollout's capture, an expert
+    product in torch, combine: gradients reach tokens, weights and the
+    router's weights, and equal those of the plain composition."""
+    tokens, k, experts, n, cols = 24, 2, 3, 64, 64
+    route, (offsets, rows, slots) = _route(tokens, k, experts, 6, dropped=0.1)
+    g = _gen(9)
+    x = torch.randn(tokens, cols, generator=g).bfloat16().to(DEV).requires_grad_()
+    w = (0.2 * torch.randn(experts, n, cols, generator=g)).bfloat16().to(DEV).requires_grad_()
+    p = torch.softmax(torch.randn(tokens, k, generator=g), 1).to(DEV).requires_grad_()
+    cache = ops.capture(ops.moe_dispatch(x.detach(), route), route.offsets)
+    xs = ops.moe_dispatch(x, route)
+    q = ops.trace_fake_quant(xs, cache)
+    parts = [q[offsets[e]:offsets[e + 1]] @ w[e].t() for e in range(experts)]
+    y = torch.cat(parts + [q.new_zeros(int(offsets[-1] - offsets[-2]), n)])
+    out = ops.moe_combine(y, route, p)
+    do = torch.randn(tokens, n, generator=g).bfloat16().to(DEV)
+    dx, dw, dp = torch.autograd.grad(out, (x, w, p), do)
+    # the same steps by hand from the library's own intermediate values
+    d = ref.f64(do)
+    live = rows >= 0
+    yr = np.where(live[..., None], ref.f64(y)[np.maximum(rows, 0)], 0.0)
+    dots = d[:, None, :] * yr
+    assert np.all(np.abs(ref.f64(dp) - dots.sum(-1)) <= (n + 5) * 2.0 ** -24 * np.abs(dots).sum(-1))
+    pd = ref.f64(p)
+    dy = np.zeros((tokens * k, n))
+    s = slots[slots >= 0]
+    dy[slots >= 0] = d[s // k] * pd.reshape(-1)[s][:, None]
+    dyb = torch.from_numpy(dy).float().bfloat16().double().numpy()  # rounded as the library does
+    wd, qd = ref.f64(w), ref.f64(q)
+    mask = ref.f64(torch.autograd.grad(ops.trace_fake_quant(z := xs.detach().requires_grad_(), cache),
+                                       z, torch.ones_like(xs))[0])
+    dq, dqm = np.zeros((tokens * k, cols)), np.zeros((tokens * k, cols))
+    for e in range(experts):
+        lo, hi = offsets[e], offsets[e + 1]
+        dq[lo:hi], dqm[lo:hi] = dyb[lo:hi] @ wd[e], np.abs(dyb[lo:hi]) @ np.abs(wd[e])
+        we, wm = dyb[lo:hi].T @ qd[lo:hi], np.abs(dyb[lo:hi]).T @ np.abs(qd[lo:hi])
+        # dy is off by half a step of bf16 where its product lies at a border
+        assert np.all(np.abs(ref.f64(dw)[e] - we) <= 2.0 ** -8 * np.abs(we) + 2.0 ** -7 * wm)
+    dq, dqm = dq * mask, dqm * mask
+    want = np.where(live[..., None], dq[np.maximum(rows, 0)], 0.0).sum(1)
+    mag = np.where(live[..., None], dqm[np.maximum(rows, 0)], 0.0).sum(1)
+    # dy (2^-8), the product's rounding (2^-8) and the sum's (2^-8), each of the magnitudes
+    assert np.all(np.abs(ref.f64(dx) - want) <= 3.1 * 2.0 ** -8 * mag)
