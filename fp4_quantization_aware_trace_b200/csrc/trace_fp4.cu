@@ -59,6 +59,7 @@
 // in csrc/*.cuh, included below inside this file's anonymous namespace (one
 // translation unit): common.cuh (shared device helpers), nvfp4.cuh, mx.cuh,
 // mismatch.cuh, util.cuh.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -289,6 +290,110 @@ int moe_sort_launch(const ID* ids, uint32_t slots, uint32_t E, int64_t* offsets,
   return cudaLaunchKernelEx(&cfg, k_moe_place<ID>, ids, slots, E,
                             (const uint32_t*)(chunks > 1 ? counts : nullptr), offsets, rows,
                             slot_of) == cudaSuccess
+             ? TRACE_OK
+             : TRACE_ERR_CUDA;
+}
+
+// cuTensorMapEncodeTiled, from the driver that the runtime has loaded.
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = nullptr;  // benign race: same value
+  if (fn == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn = (EncodeTiled)p;
+  }
+  return fn;
+}
+
+// [rows, bytes] codes, copied in boxes of box_rows x 128 bytes (128-byte
+// swizzle); what lies outside the array arrives as zeros.
+int code_map(CUtensorMap* map, const uint8_t* codes, uint64_t rows, uint64_t bytes,
+             uint32_t box_rows) {
+  const EncodeTiled encode = encode_tiled();
+  if (encode == nullptr) return TRACE_ERR_CUDA;
+  const cuuint64_t dims[2] = {bytes, rows}, strides[1] = {bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)kMmStageBytes, box_rows}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)codes, dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? TRACE_OK
+             : TRACE_ERR_CUDA;
+}
+
+template <bool MX>
+int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gscale,
+                  int64_t rows, int64_t cols, int32_t groups, const int64_t* offs, int a_layout,
+                  const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gscale,
+                  int64_t n, int32_t matrices, int w_layout, uint16_t* out, cudaStream_t stream) {
+  constexpr uint32_t kAtoms = MX ? 2 : 4;
+  constexpr uint32_t kSmem = 227u * 1024u;
+  const int sms = sm_count();
+  if (sms <= 0) return TRACE_ERR_CUDA;
+  MmShape sh;
+  sh.rows = rows;
+  sh.n = n;
+  sh.cols = (uint32_t)cols;
+  sh.scols = (uint32_t)(cols / (MX ? 32 : 16));
+  sh.groups = groups;
+  sh.matrices = matrices;
+  const int64_t mean = (rows + groups - 1) / groups;
+  sh.nt = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : 192;
+  sh.n_tiles = (uint32_t)((n + kMmM - 1) / kMmM);
+  sh.ksteps = (uint32_t)((cols + 2 * kMmStageBytes - 1) / (2 * kMmStageBytes));
+  sh.accs = 2;
+  const uint32_t rb = (sh.nt + 127) / 128;
+  const uint32_t stage =
+      ((kMmM + sh.nt) * kMmStageBytes + kAtoms * 512u * (1 + rb) + 1023u) & ~1023u;
+  const uint32_t fixed = 1024u + 4 * 32 * 40 * 2 + 4u * (uint32_t)(groups + 1);
+  sh.stages = (kSmem - 1024u - fixed) / stage;
+  if (sh.stages > (uint32_t)kMmMaxStages) sh.stages = kMmMaxStages;
+  sh.sf_slots = (kMmTmemCols - sh.accs * ((sh.nt + 31u) & ~31u)) / (4u * kAtoms * (1 + rb));
+  if (sh.sf_slots > sh.stages) sh.sf_slots = sh.stages;
+  sh.a_tiled = a_layout == TRACE_SCALES_TILED_128x4;
+  sh.w_tiled = w_layout == TRACE_SCALES_TILED_128x4;
+  sh.a_bytes = !sh.a_tiled && (sh.scols % 4 != 0 || !aligned(a_scales, 4));
+  sh.w_bytes = !sh.w_tiled && (sh.scols % 4 != 0 || !aligned(w_scales, 4));
+  sh.out16 = n % 8 == 0;
+  const long double tiles =
+      ((long double)rows / sh.nt + groups) * (long double)sh.n_tiles;
+  if (tiles >= 2147483648.0L) return TRACE_ERR_SHAPE;
+  CUtensorMap a_map, w_map;
+  int st = code_map(&a_map, a_codes, (uint64_t)rows, (uint64_t)cols / 2, sh.nt);
+  if (!st) st = code_map(&w_map, w_codes, (uint64_t)n * matrices, (uint64_t)cols / 2, kMmM);
+  if (st) return st;
+  static bool attr_set[kMaxDevices];  // benign race: same value
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TRACE_ERR_CUDA;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(k_matmul<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kSmem - 1024u)) != cudaSuccess)
+      return TRACE_ERR_CUDA;
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  const uint32_t most = groups == 1 ? (uint32_t)tiles : (uint32_t)sms;
+  cfg.gridDim = dim3(most < (uint32_t)sms ? (most > 0 ? most : 1) : (uint32_t)sms);
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = sh.stages * stage + fixed;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_matmul<MX>, a_map, w_map, a_scales, w_scales, a_gscale,
+                            w_gscale, groups > 1 ? offs : (const int64_t*)nullptr, sh, out) ==
+                 cudaSuccess
              ? TRACE_OK
              : TRACE_ERR_CUDA;
 }
@@ -982,19 +1087,12 @@ static int matmul_impl(bool mx, const uint8_t* a_codes, const uint8_t* a_scales,
       (a_layout && !aligned(a_scales, 16)) || (w_layout && !aligned(w_scales, 16)) ||
       !aligned(a_gscale, 4) || !aligned(w_gscale, 4) || !aligned(offs, 8))
     return TRACE_ERR_ALIGN;
-  MmShape sh;
-  sh.rows = rows;
-  sh.n = n;
-  sh.cols = (uint32_t)cols;
-  sh.groups = num_groups;
-  sh.matrices = num_matrices;
-  sh.a_tiled = a_layout;
-  sh.w_tiled = w_layout;
-  int grid;
-  if ((st = moe_grid(((u64)rows * (u64)n + 31) / 32, &grid))) return st;
-  const int64_t* o = num_groups > 1 ? offs : nullptr;
-  return launch(mx ? k_matmul_simple<true> : k_matmul_simple<false>, grid, (cudaStream_t)stream,
-                a_codes, a_scales, a_gscale, o, w_codes, w_scales, w_gscale, sh, out);
+  return mx ? matmul_launch<true>(a_codes, a_scales, nullptr, rows, cols, num_groups, offs,
+                                  a_layout, w_codes, w_scales, nullptr, n, num_matrices, w_layout,
+                                  out, (cudaStream_t)stream)
+            : matmul_launch<false>(a_codes, a_scales, a_gscale, rows, cols, num_groups, offs,
+                                   a_layout, w_codes, w_scales, w_gscale, n, num_matrices,
+                                   w_layout, out, (cudaStream_t)stream);
 }
 
 int trace_fp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gscale,
@@ -1006,6 +1104,22 @@ int trace_fp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const floa
   return matmul_impl(false, a_codes, a_scales, a_gscale, rows, cols, num_groups,
                      group_row_offsets, a_scale_layout, w_codes, w_scales, w_gscale, n,
                      num_matrices, w_scale_layout, out, stream);
+}
+
+int trace_matmul_status(void* stream) {
+  if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return TRACE_ERR_CUDA;
+  uint32_t word = 0;
+  if (cudaMemcpyFromSymbolAsync(&word, g_matmul_gave_up, 4, 0, cudaMemcpyDeviceToHost,
+                                (cudaStream_t)stream) != cudaSuccess ||
+      cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess)
+    return TRACE_ERR_CUDA;
+  if (word == 0) return TRACE_OK;
+  const uint32_t zero = 0;
+  if (cudaMemcpyToSymbolAsync(g_matmul_gave_up, &zero, 4, 0, cudaMemcpyHostToDevice,
+                              (cudaStream_t)stream) != cudaSuccess ||
+      cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess)
+    return TRACE_ERR_CUDA;
+  return TRACE_ERR_TIMEOUT;
 }
 
 int trace_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows, int64_t cols,

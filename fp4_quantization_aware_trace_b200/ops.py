@@ -130,6 +130,8 @@ def library() -> ctypes.CDLL:
         lib.trace_fp4_matmul.restype = ctypes.c_int
         lib.trace_mx_matmul.argtypes = [P, P, i64, i64, i32, P, i32, P, P, i64, i32, i32, P, P]
         lib.trace_mx_matmul.restype = ctypes.c_int
+        lib.trace_matmul_status.argtypes = [P]
+        lib.trace_matmul_status.restype = ctypes.c_int
         lib.trace_capture_status.argtypes = [P, P]
         lib.trace_capture_status.restype = ctypes.c_int
         _lib = lib
@@ -1031,3 +1033,13 @@ def mx_matmul(a: MxCapture, w: MxCapture, cols: int | None = None,
         cols = int(w.scales.shape[1]) * 32
     rows = None if cols is None else a.codes.numel() * 2 // cols
     return _matmul(a, w, cols, offsets, _groups(offsets, rows), groups, out, stream, "mxfp4")
+
+
+def matmul_status(stream=None) -> bool:
+    """True when no product on the current device has given up a wait since
+    the last check (trace_matmul_status: waits for the stream)."""
+    st = library().trace_matmul_status(_stream(stream))
+    if st == TRACE_ERR_TIMEOUT:
+        return False
+    _check(st, "trace_matmul_status")
+    return True

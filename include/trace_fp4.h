@@ -555,6 +555,14 @@ int trace_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t row
                     const uint8_t* w_codes, const uint8_t* w_scales, int64_t n,
                     int32_t num_matrices, int32_t w_scale_layout, uint16_t* out, void* stream);
 
+/* Whether a product on the current device has given up a wait for its own
+ * copies since the last check (every wait is bounded; none is expected to
+ * run out): waits for the work queued on `stream`, reads and clears one word
+ * of the library per GPU and returns TRACE_ERR_TIMEOUT if it was set (the
+ * outputs since the last check are then not valid), else TRACE_OK.  Not for
+ * use during stream capture (it synchronises). */
+int trace_matmul_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif
