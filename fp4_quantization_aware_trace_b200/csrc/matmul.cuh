@@ -14,20 +14,24 @@
 // column j, tensor-memory column = token.
 //
 // One persistent CTA per SM walks tiles; its warps are specialised:
-//   warp 0  copies both operands' codes by TMA, 256 k-elements (128 bytes per
-//           row, 128-byte swizzle) per stage of a shared-memory ring;
-//   warps 2, 3 copy the block scales into the ring in the 128 x 4 tiled
-//           order the tensor core wants, from either layout and at any row
-//           (a group starts anywhere), and zero what lies past the last k;
-//   warp 1  moves a stage's scales to tensor memory and issues its products;
-//   warps 4-7 read finished accumulators and write bf16 rows of out, while
-//           the next tile runs on the other accumulator.
+//   warp 0     copies both operands' codes by TMA, 256 k-elements (128 bytes
+//              per row, 128-byte swizzle) per stage of a shared-memory ring,
+//              and tiled scales whose 128-row block is the tile's own;
+//   warps 8-11 copy all other scales into the ring in the 128 x 4 tiled order
+//              the tensor core wants, from either layout and at any row (a
+//              group starts anywhere), and zero what lies past the last k;
+//   warp 1     moves a stage's scales to tensor memory and issues its
+//              products;
+//   warps 4-7  read finished accumulators and write bf16 rows of out, while
+//              the next tile runs on the other accumulator.
+// Each role is one warp that runs alone on its scheduler, so a stage costs it
+// its instructions' latencies: ring positions are counters and not quotients,
+// and the loops over a stage's parts are unrolled.
 #pragma once
 
-constexpr int kMmThreads = 256;
+constexpr int kMmThreads = 384;
 constexpr int kMmM = 128;            // w rows of a tile
 constexpr int kMmStageBytes = 128;   // code bytes per row and stage: 256 elements
-constexpr int kMmScaleLag = 3;       // stages the scale copies run ahead (<= stages - 1)
 constexpr int kMmMaxStages = 8;
 constexpr uint32_t kMmTmemCols = 512;
 // Polls of one wait before a CTA gives up (each try_wait itself suspends):
@@ -105,13 +109,21 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// bytes <= 4 (16) of a word; the rest of it becomes zero.
+// A contiguous copy, counted on the stage's barrier (whose expected bytes
+// include it); addresses and size are multiples of 16.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// `bytes` <= 4 of a word; the rest of it becomes zero.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // Shared-memory matrix descriptors: codes with 128-byte rows in the 128-byte
@@ -177,6 +189,17 @@ __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// A position in a ring of `size` slots and the parity of its current round.
+struct Ring {
+  uint32_t at = 0, parity = 0;
+  __device__ __forceinline__ void next(uint32_t size) {
+    if (++at == size) {
+      at = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Tiles
 // ---------------------------------------------------------------------------
@@ -215,7 +238,7 @@ __device__ __forceinline__ MmTile mm_tile(uint32_t t, const uint32_t* first_tile
   return m;
 }
 
-// first_tile[0 .. groups] by a scan over the CTA (256 threads).
+// first_tile[0 .. groups] by a scan over the CTA.
 __device__ __forceinline__ void mm_table(uint32_t* first_tile, uint32_t* warp_sum,
                                          const int64_t* offs, const MmShape& sh) {
   const uint32_t lane = threadIdx.x % 32u, warp = threadIdx.x / 32u;
@@ -249,97 +272,92 @@ __device__ __forceinline__ void mm_table(uint32_t* first_tile, uint32_t* warp_su
 }
 
 // ---------------------------------------------------------------------------
-// Scales of one 128-row block for one stage, into ATOMS atoms of 512 bytes
-// (128 rows x 4 scale columns each).  `half` picks which rows (or atoms) this
-// warp copies: two warps share the work.
+// Scales of one 128-row block for one stage: ATOMS pieces of 512 bytes (128
+// rows x 4 scale columns), `apart` bytes from one to the next.  Each of the
+// four scale warps copies a quarter of the rows, one 4-byte word per lane and
+// piece.
 // ---------------------------------------------------------------------------
 struct ScaleSrc {
-  const uint8_t* base;
-  const uint8_t* row[2];  // this lane's rows 32 (2 half + q) + lane; null: not in the array
-  uint32_t step;          // bytes from one group of 4 columns to the next
-  bool words16;           // the block is one of the tiled layout's own
-  bool bytes;             // no 4-byte alignment
+  const uint8_t* row;  // this lane's row (null: past the array's end)
+  uint32_t step;       // bytes from one group of 4 columns to the next
+  bool bulk;           // the block is one of the tiled layout's own: TMA's work
+  bool bytes;          // rows without 4-byte alignment
 };
+
+// Whether the copy engine takes stage k of a block: 512-byte pieces as they
+// are, none of them with columns past the last.
+__device__ __forceinline__ bool scales_bulk(bool tiled, int64_t row0) {
+  return tiled && row0 % 128 == 0;
+}
 
 __device__ __forceinline__ ScaleSrc scale_src(const uint8_t* base, bool tiled, bool bytes,
                                               int64_t row0, int64_t rows, uint32_t scols,
-                                              uint32_t half, uint32_t lane) {
+                                              uint32_t quarter, uint32_t lane) {
   ScaleSrc s;
-  s.base = base;
   s.bytes = bytes;
   s.step = tiled ? 512u : 4u;
-  s.words16 = tiled && row0 % 128 == 0;
+  s.bulk = scales_bulk(tiled, row0);
   const uint32_t ct = (scols + 3u) / 4u;
-#pragma unroll
-  for (uint32_t q = 0; q < 2u; ++q) {
-    const int64_t r = row0 + 32u * (2u * half + q) + lane;
-    s.row[q] = nullptr;
-    if (r < rows)
-      s.row[q] = tiled ? base + (size_t)(r / 128) * ct * 512u + (size_t)(r % 32) * 16u +
-                             (size_t)(r % 128 / 32) * 4u
-                       : base + (size_t)r * scols;
-  }
+  const int64_t r = row0 + 32u * quarter + lane;
+  s.row = r >= rows ? nullptr
+          : tiled   ? base + (size_t)(r / 128) * ct * 512u + (size_t)(r % 32) * 16u +
+                        (size_t)(r % 128 / 32) * 4u
+                    : base + (size_t)r * scols;
   return s;
 }
 
+// `at`: this lane's word of the first piece.
 template <int ATOMS>
-__device__ __forceinline__ void copy_scales(const ScaleSrc& s, int64_t row0, uint32_t dst,
-                                            uint32_t dst_step, uint32_t kstep, uint32_t scols,
-                                            uint32_t half, uint32_t lane) {
+__device__ __forceinline__ void copy_scales(const ScaleSrc& s, const uint8_t* base, uint32_t at,
+                                            uint32_t apart, uint32_t k, uint32_t scols) {
+  const uint32_t c0 = k * (4u * ATOMS);
+  if (c0 + 4u * ATOMS <= scols && !s.bytes) {
+    if (s.bulk || s.row == nullptr) return;  // rows past the end reach no output
+    const uint8_t* from = s.row + (size_t)(k * ATOMS) * s.step;
 #pragma unroll
+    for (uint32_t j = 0; j < (uint32_t)ATOMS; ++j) cp_async4(at + j * apart, from + j * s.step, 4u);
+    return;
+  }
   for (uint32_t j = 0; j < (uint32_t)ATOMS; ++j) {
-    const uint32_t c4 = kstep * ATOMS + j;  // group of 4 scale columns
-    const uint32_t valid = 4u * c4 >= scols ? 0u : min(4u, scols - 4u * c4);
-    const uint32_t to = dst + j * dst_step;
-    if (s.words16 && valid == 4u) {
-      if (j % 2u == half) {
-        const uint32_t ct = (scols + 3u) / 4u;
-        cp_async16(to + 16u * lane, s.base + ((size_t)(row0 / 128) * ct + c4) * 512u + 16u * lane);
-      }
-      continue;
-    }
-#pragma unroll
-    for (uint32_t q = 0; q < 2u; ++q) {
-      const uint32_t at = to + 16u * lane + 4u * (2u * half + q);
-      const uint32_t take = s.row[q] != nullptr ? valid : 0u;
-      if (!s.bytes) {
-        cp_async4(at, take ? s.row[q] + (size_t)c4 * s.step : s.base, take);
-      } else {
-        uint32_t w = 0u;
-        for (uint32_t i = 0; i < take; ++i) w |= (uint32_t)s.row[q][4u * c4 + i] << (8u * i);
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
-      }
+    const uint32_t c = c0 + 4u * j;
+    const uint32_t take = s.row == nullptr || c >= scols ? 0u : min(4u, scols - c);
+    if (!s.bytes) {
+      cp_async4(at + j * apart, take ? s.row + (size_t)(c / 4u) * s.step : base, take);
+    } else {
+      uint32_t w = 0u;
+      for (uint32_t i = 0; i < take; ++i) w |= (uint32_t)s.row[c + i] << (8u * i);
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + j * apart), "r"(w) : "memory");
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// The kernel
+// The kernel; RB: 128-row blocks of token scales (1 up to 128 tokens, else 2)
 // ---------------------------------------------------------------------------
-template <bool MX>
+template <bool MX, int RB>
 __global__ void __launch_bounds__(kMmThreads, 1)
     k_matmul(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap w_map,
              const uint8_t* __restrict__ as, const uint8_t* __restrict__ ws,
              const float* __restrict__ ag, const float* __restrict__ wg,
              const int64_t* __restrict__ offs, MmShape sh, uint16_t* __restrict__ out) {
   constexpr uint32_t ATOMS = MX ? 2 : 4;  // groups of 4 scale columns per stage
+  constexpr uint32_t w_code = kMmM * kMmStageBytes;
+  constexpr uint32_t block_bytes = ATOMS * 512u;  // a block's scales per stage
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) u64 full[kMmMaxStages], empty[kMmMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base_s, warp_sum[kMmThreads / 32];
   __shared__ volatile uint32_t gave_up;
   const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
-  const uint32_t rb = (sh.nt + 127u) / 128u;  // 128-row blocks of token scales
-  const uint32_t w_code = kMmM * kMmStageBytes, x_code = sh.nt * kMmStageBytes;
-  const uint32_t stage_bytes = w_code + x_code + ATOMS * 512u * (1u + rb);
+  const uint32_t x_code = sh.nt * kMmStageBytes;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t stage_at = (stage_bytes + 1023u) & ~1023u;
+  const uint32_t stage_at = (w_code + x_code + block_bytes * (1u + RB) + 1023u) & ~1023u;
   uint8_t* after = smem_raw + (ring - smem_u32(smem_raw)) + sh.stages * stage_at;
   uint16_t* turn = reinterpret_cast<uint16_t*>(after);               // [4][32][40] bf16
   uint32_t* first_tile = reinterpret_cast<uint32_t*>(after + 4 * 32 * 40 * 2);
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < sh.stages; ++s) {
-      mbar_init(smem_u32(&full[s]), 3);  // the TMA thread and two scale warps
+      mbar_init(smem_u32(&full[s]), 1 + 128);  // the TMA thread and the scale lanes
       mbar_init(smem_u32(&empty[s]), 1);
     }
     for (uint32_t a = 0; a < 2; ++a) {
@@ -364,140 +382,153 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   const uint32_t tmem = tmem_base_s;
   const uint32_t tiles = first_tile[sh.groups] * sh.n_tiles;
   const uint32_t acc_cols = (sh.nt + 31u) & ~31u;
-  const uint32_t sf_cols = 4u * ATOMS * (1u + rb);  // tensor-memory columns of a stage's scales
+  constexpr uint32_t sf_cols = 4u * ATOMS * (1u + RB);  // tensor-memory columns of a stage's scales
   const uint32_t sf_base = tmem + sh.accs * acc_cols;
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t i = 0;  // stages filled so far
+      Ring r;
+      r.parity = 1u;  // the first round finds every slot empty
       bool ok = true;
+      const uint32_t c4s = (sh.scols + 3u) / 4u, bulk_steps = sh.scols / (4u * ATOMS);
       for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const MmTile m = mm_tile(t, first_tile, offs, sh);
         if (!m.product) continue;
-        const int32_t wr = (int32_t)(m.group * sh.n + m.j0);
-        for (uint32_t k = 0; k < sh.ksteps; ++k, ++i) {
-          const uint32_t s = i % sh.stages;
-          if (i >= sh.stages &&
-              !(ok = mm_wait(smem_u32(&empty[s]), (i / sh.stages - 1u) & 1u, &gave_up)))
-            break;
-          const uint32_t at = ring + s * stage_at, bar = smem_u32(&full[s]);
-          mbar_expect(bar, w_code + x_code);
-          tma_load_2d(at, &w_map, (int32_t)(k * kMmStageBytes), wr, bar);
+        const int64_t wr = m.group * sh.n + m.j0;
+        const bool w_bulk = scales_bulk(sh.w_tiled, wr), x_bulk = scales_bulk(sh.a_tiled, m.row0);
+        const bool two = RB == 2 && m.tokens > 128u;
+        const uint8_t* w_from = ws + (size_t)(wr / 128) * c4s * 512u;
+        const uint8_t* x_from = as + (size_t)(m.row0 / 128) * c4s * 512u;
+        const uint32_t bulk_bytes = (w_bulk ? block_bytes : 0u) +
+                                    (x_bulk ? (two ? 2u : 1u) * block_bytes : 0u);
+        for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages)) {
+          const uint32_t bar = smem_u32(&full[r.at]), at = ring + r.at * stage_at;
+          if (!(ok = mm_wait(smem_u32(&empty[r.at]), r.parity, &gave_up))) break;
+          const bool bulk = k < bulk_steps;
+          mbar_expect(bar, w_code + x_code + (bulk ? bulk_bytes : 0u));
+          tma_load_2d(at, &w_map, (int32_t)(k * kMmStageBytes), (int32_t)wr, bar);
           tma_load_2d(at + w_code, &a_map, (int32_t)(k * kMmStageBytes), (int32_t)m.row0, bar);
+          if (bulk) {
+            const uint32_t sc = at + w_code + x_code;
+            if (w_bulk) bulk_copy(sc, w_from + (size_t)k * block_bytes, block_bytes, bar);
+            if (x_bulk) {
+              bulk_copy(sc + block_bytes, x_from + (size_t)k * block_bytes, block_bytes, bar);
+              if (two)
+                bulk_copy(sc + 2u * block_bytes, x_from + (size_t)c4s * 512u + (size_t)k * block_bytes,
+                          block_bytes, bar);
+            }
+          }
         }
       }
       if (!ok)  // let the copies in flight land before the CTA leaves
         for (int z = 0; z < 1000; ++z) __nanosleep(1000);
     }
-  } else if (warp == 2 || warp == 3) {
-    const uint32_t half = warp - 2u;
-    uint32_t i = 0;
+  } else if (warp >= 8) {
+    const uint32_t quarter = warp - 8u;
+    Ring r;
+    r.parity = 1u;
     bool ok = true;
-    const auto publish = [&](uint32_t done) {  // this warp's copies of stage number `done` are in
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&full[done % sh.stages]));
-    };
     for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const MmTile m = mm_tile(t, first_tile, offs, sh);
       if (!m.product) continue;
-      const int64_t wr = (int64_t)m.group * sh.n + m.j0;
+      const int64_t wr = m.group * sh.n + m.j0;
       const ScaleSrc sw = scale_src(ws, sh.w_tiled, sh.w_bytes, wr, sh.n * sh.matrices, sh.scols,
-                                    half, lane);
-      const ScaleSrc s0 = scale_src(as, sh.a_tiled, sh.a_bytes, m.row0, sh.rows, sh.scols, half,
+                                    quarter, lane);
+      const ScaleSrc s0 = scale_src(as, sh.a_tiled, sh.a_bytes, m.row0, sh.rows, sh.scols, quarter,
                                     lane);
-      const bool two = m.tokens > 128u;
-      const ScaleSrc s1 = scale_src(as, sh.a_tiled, sh.a_bytes, m.row0 + 128, two ? sh.rows : 0,
-                                    sh.scols, half, lane);
-      for (uint32_t k = 0; k < sh.ksteps; ++k, ++i) {
-        const uint32_t s = i % sh.stages;
-        if (i >= sh.stages &&
-            !(ok = mm_wait(smem_u32(&empty[s]), (i / sh.stages - 1u) & 1u, &gave_up)))
-          break;
-        const uint32_t at = ring + s * stage_at + w_code + x_code;
-        copy_scales<ATOMS>(sw, wr, at, 512u, k, sh.scols, half, lane);
-        const uint32_t ax = at + ATOMS * 512u;
-        copy_scales<ATOMS>(s0, m.row0, ax, 512u * rb, k, sh.scols, half, lane);
-        if (two) copy_scales<ATOMS>(s1, m.row0 + 128, ax + 512u, 512u * rb, k, sh.scols, half, lane);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (i >= (uint32_t)kMmScaleLag) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(kMmScaleLag) : "memory");
-          publish(i - kMmScaleLag);
+      const bool two = RB == 2 && m.tokens > 128u;
+      const ScaleSrc s1 = scale_src(as, sh.a_tiled, sh.a_bytes, m.row0 + 128, sh.rows, sh.scols,
+                                    quarter, lane);
+      const uint32_t word = w_code + x_code + 16u * lane + 4u * quarter;
+      for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages)) {
+        if (!(ok = mm_wait(smem_u32(&empty[r.at]), r.parity, &gave_up))) break;
+        const uint32_t at = ring + r.at * stage_at + word, bar = smem_u32(&full[r.at]);
+        copy_scales<ATOMS>(sw, ws, at, 512u, k, sh.scols);
+        copy_scales<ATOMS>(s0, as, at + block_bytes, 512u, k, sh.scols);
+        if (two) copy_scales<ATOMS>(s1, as, at + 2u * block_bytes, 512u, k, sh.scols);
+        if (sw.bytes || s0.bytes) {  // plain stores: nothing that arrives by itself
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          mbar_arrive(bar);
+        } else {
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar)
+                       : "memory");
         }
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (ok)
-      for (uint32_t d = i > (uint32_t)kMmScaleLag ? i - kMmScaleLag : 0u; d < i; ++d) publish(d);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
     if (lane == 0) {
-      uint32_t i = 0, n_acc = 0;  // stages used, tiles begun
+      Ring r, acc, sf, sf_last;  // sf_last: the stage that used the scale slot before
+      acc.parity = 1u;
+      uint32_t begun = 0;  // scale slots used so far, up to sf_slots
       bool ok = true;
+      Ring last;
+      bool any = false;
       for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const MmTile m = mm_tile(t, first_tile, offs, sh);
         if (!m.product) continue;
-        const uint32_t a = n_acc % sh.accs;
-        if (n_acc >= sh.accs &&
-            !(ok = mm_wait(smem_u32(&acc_empty[a]), (n_acc / sh.accs - 1u) & 1u, &gave_up)))
-          break;
-        ++n_acc;
-        const uint32_t d = tmem + a * acc_cols;
+        if (!(ok = mm_wait(smem_u32(&acc_empty[acc.at]), acc.parity, &gave_up))) break;
+        const uint32_t d = tmem + acc.at * acc_cols;
         const uint32_t idesc = mm_idesc<MX>((m.tokens + 15u) & ~15u);
-        const uint32_t blocks = m.tokens > 128u ? 2u : 1u;
-        for (uint32_t k = 0; k < sh.ksteps; ++k, ++i) {
-          const uint32_t s = i % sh.stages;
+        const bool two = RB == 2 && m.tokens > 128u;
+        uint32_t left = sh.cols;
+        for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages), sf.next(sh.sf_slots)) {
           // the scale slot's last reader must be done
-          if (i >= sh.sf_slots) {
-            const uint32_t p = i - sh.sf_slots;
-            if (!(ok = mm_wait(smem_u32(&empty[p % sh.stages]), (p / sh.stages) & 1u, &gave_up)))
-              break;
+          if (begun == sh.sf_slots) {
+            if (!(ok = mm_wait(smem_u32(&empty[sf_last.at]), sf_last.parity, &gave_up))) break;
+            sf_last.next(sh.stages);
+          } else {
+            ++begun;
           }
-          if (!(ok = mm_wait(smem_u32(&full[s]), (i / sh.stages) & 1u, &gave_up))) break;
+          if (!(ok = mm_wait(smem_u32(&full[r.at]), r.parity, &gave_up))) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t at = ring + s * stage_at;
-          const uint32_t sf = sf_base + (i % sh.sf_slots) * sf_cols;
-          const uint32_t sfx = sf + 4u * ATOMS;
-          const uint32_t asc = at + w_code + x_code, axs = asc + ATOMS * 512u;
+          // scales written by cp.async and plain stores: seen by the copy below
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          const uint32_t at = ring + r.at * stage_at;
+          const uint32_t slot = sf_base + sf.at * sf_cols;
+          const u64 sd = scale_desc(at + w_code + x_code);
+#pragma unroll
           for (uint32_t j = 0; j < ATOMS; ++j) {
-            scales_to_tmem(sf + 4u * j, scale_desc(asc + 512u * j));
-            for (uint32_t b = 0; b < blocks; ++b)
-              scales_to_tmem(sfx + 4u * (j * rb + b), scale_desc(axs + 512u * (j * rb + b)));
+            scales_to_tmem(slot + 4u * j, sd + 32u * j);
+            scales_to_tmem(slot + 4u * ATOMS + 4u * RB * j, sd + 32u * (ATOMS + j));
+            if (two)
+              scales_to_tmem(slot + 4u * ATOMS + 4u * (RB * j + 1u), sd + 32u * (2u * ATOMS + j));
           }
-          const uint32_t left = sh.cols - k * 256u;
-          const uint32_t mmas = left >= 256u ? 4u : (left + 63u) / 64u;
           const u64 da = code_desc(at), db = code_desc(at + w_code);
-          for (uint32_t j = 0; j < mmas; ++j) {
-            const uint32_t c = MX ? j / 2u : j;  // atom of this product's scales
+#pragma unroll
+          for (uint32_t j = 0; j < 4u; ++j) {
+            const uint32_t c = MX ? j / 2u : j;  // piece with this product's scales
             const uint32_t id = MX ? (j & 1u) * 2u : 0u;
-            mma_fp4<MX>(d, da + 2u * j, db + 2u * j, idesc | (id << 4) | (id << 29), sf + 4u * c,
-                        sfx + 4u * rb * c, (k | j) != 0u);
+            if (left > 64u * j)
+              mma_fp4<MX>(d, da + 2u * j, db + 2u * j, idesc | (id << 4) | (id << 29),
+                          slot + 4u * c, slot + 4u * ATOMS + 4u * RB * c, (k | j) != 0u);
           }
-          mma_commit(smem_u32(&empty[s]));
+          left -= 256u;  // wraps only after the last step
+          mma_commit(smem_u32(&empty[r.at]));
+          last = r;
+          any = true;
         }
-        if (ok) mma_commit(smem_u32(&acc_full[a]));
+        if (!ok) break;
+        mma_commit(smem_u32(&acc_full[acc.at]));
+        acc.next(sh.accs);
       }
       // the products in flight must end before tensor memory is freed
-      if (i > 0) {
-        const uint32_t p = i - 1u;
-        mm_wait(smem_u32(&empty[p % sh.stages]), (p / sh.stages) & 1u, &gave_up);
-      }
+      if (any) mm_wait(smem_u32(&empty[last.at]), last.parity, &gave_up);
     }
-  } else {
+  } else if (warp >= 4) {
     const uint32_t q = warp - 4u;  // this warp's 32 lanes of tensor memory
     uint16_t* mine = turn + q * 32u * 40u;
-    uint32_t n_acc = 0;
+    Ring acc;
     bool ok = true;
     for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const MmTile m = mm_tile(t, first_tile, offs, sh);
-      const uint32_t a = n_acc % sh.accs;
       OutScale scale{1.0f, 1.0f, 1.0f};
       if (m.product) {
-        if (!(ok = mm_wait(smem_u32(&acc_full[a]), (n_acc / sh.accs) & 1u, &gave_up))) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        ++n_acc;
         if (!MX) scale = make_out_scale(ag[m.group], wg[m.group]);
+        if (!(ok = mm_wait(smem_u32(&acc_full[acc.at]), acc.parity, &gave_up))) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       }
-      const uint32_t d = tmem + a * acc_cols + (q << 21);
+      const uint32_t d = tmem + acc.at * acc_cols + (q << 21);
       const uint32_t j0 = m.j0 + 32u * q;
       for (uint32_t c0 = 0; c0 < m.tokens; c0 += 32u) {
         uint32_t v[32];
@@ -533,7 +564,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       if (m.product) {
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&acc_empty[a]));
+        if (lane == 0) mbar_arrive(smem_u32(&acc_empty[acc.at]));
+        acc.next(sh.accs);
       }
     }
   }

@@ -375,7 +375,9 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TRACE_ERR_CUDA;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(k_matmul<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(k_matmul<MX, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kSmem - 1024u)) != cudaSuccess ||
+        cudaFuncSetAttribute(k_matmul<MX, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kSmem - 1024u)) != cudaSuccess)
       return TRACE_ERR_CUDA;
     attr_set[dev] = true;
@@ -391,7 +393,7 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_matmul<MX>, a_map, w_map, a_scales, w_scales, a_gscale,
+  return cudaLaunchKernelEx(&cfg, rb == 1 ? k_matmul<MX, 1> : k_matmul<MX, 2>, a_map, w_map, a_scales, w_scales, a_gscale,
                             w_gscale, groups > 1 ? offs : (const int64_t*)nullptr, sh, out) ==
                  cudaSuccess
              ? TRACE_OK
