@@ -89,12 +89,24 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
                : "memory");
 }
 
+// One lane of a converged warp; ptxas knows that a branch on it leaves a
+// single thread and keeps the operands of what it issues in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0u;
+}
+
 // Bounded wait for a phase; false once any wait of the CTA has given up.
+// The lanes of a warp agree on the answer.
 __device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+  bool ok = false;
   for (uint32_t i = 0; i < kMmPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 255u && *gave_up) return false;
+    if ((ok = mbar_try_wait(bar, parity))) break;
+    if ((i & 255u) == 255u && *gave_up) break;
   }
+  if (__all_sync(0xFFFFFFFFu, ok)) return true;
   *gave_up = 1u;
   g_matmul_gave_up = 1u;
   return false;
@@ -347,7 +359,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   __shared__ __align__(8) u64 full[kMmMaxStages], empty[kMmMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base_s, warp_sum[kMmThreads / 32];
   __shared__ volatile uint32_t gave_up;
-  const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
+  const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32u, 0), lane = threadIdx.x % 32u;
   const uint32_t x_code = sh.nt * kMmStageBytes;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t stage_at = (w_code + x_code + block_bytes * (1u + RB) + 1023u) & ~1023u;
@@ -386,43 +398,42 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   const uint32_t sf_base = tmem + sh.accs * acc_cols;
 
   if (warp == 0) {
-    if (lane == 0) {
-      Ring r;
-      r.parity = 1u;  // the first round finds every slot empty
-      bool ok = true;
-      const uint32_t c4s = (sh.scols + 3u) / 4u, bulk_steps = sh.scols / (4u * ATOMS);
-      for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const MmTile m = mm_tile(t, first_tile, offs, sh);
-        if (!m.product) continue;
-        const int64_t wr = m.group * sh.n + m.j0;
-        const bool w_bulk = scales_bulk(sh.w_tiled, wr), x_bulk = scales_bulk(sh.a_tiled, m.row0);
-        const bool two = RB == 2 && m.tokens > 128u;
-        const uint8_t* w_from = ws + (size_t)(wr / 128) * c4s * 512u;
-        const uint8_t* x_from = as + (size_t)(m.row0 / 128) * c4s * 512u;
-        const uint32_t bulk_bytes = (w_bulk ? block_bytes : 0u) +
-                                    (x_bulk ? (two ? 2u : 1u) * block_bytes : 0u);
-        for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages)) {
-          const uint32_t bar = smem_u32(&full[r.at]), at = ring + r.at * stage_at;
-          if (!(ok = mm_wait(smem_u32(&empty[r.at]), r.parity, &gave_up))) break;
-          const bool bulk = k < bulk_steps;
-          mbar_expect(bar, w_code + x_code + (bulk ? bulk_bytes : 0u));
-          tma_load_2d(at, &w_map, (int32_t)(k * kMmStageBytes), (int32_t)wr, bar);
-          tma_load_2d(at + w_code, &a_map, (int32_t)(k * kMmStageBytes), (int32_t)m.row0, bar);
-          if (bulk) {
-            const uint32_t sc = at + w_code + x_code;
-            if (w_bulk) bulk_copy(sc, w_from + (size_t)k * block_bytes, block_bytes, bar);
-            if (x_bulk) {
-              bulk_copy(sc + block_bytes, x_from + (size_t)k * block_bytes, block_bytes, bar);
-              if (two)
-                bulk_copy(sc + 2u * block_bytes, x_from + (size_t)c4s * 512u + (size_t)k * block_bytes,
-                          block_bytes, bar);
-            }
+    Ring r;
+    r.parity = 1u;  // the first round finds every slot empty
+    bool ok = true;
+    const uint32_t c4s = (sh.scols + 3u) / 4u, bulk_steps = sh.scols / (4u * ATOMS);
+    for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const MmTile m = mm_tile(t, first_tile, offs, sh);
+      if (!m.product) continue;
+      const int64_t wr = m.group * sh.n + m.j0;
+      const bool w_bulk = scales_bulk(sh.w_tiled, wr), x_bulk = scales_bulk(sh.a_tiled, m.row0);
+      const bool two = RB == 2 && m.tokens > 128u;
+      const uint8_t* w_from = ws + (size_t)(wr / 128) * c4s * 512u;
+      const uint8_t* x_from = as + (size_t)(m.row0 / 128) * c4s * 512u;
+      const uint32_t bulk_bytes = (w_bulk ? block_bytes : 0u) +
+                                  (x_bulk ? (two ? 2u : 1u) * block_bytes : 0u);
+      for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages)) {
+        const uint32_t bar = smem_u32(&full[r.at]), at = ring + r.at * stage_at;
+        if (!(ok = mm_wait(smem_u32(&empty[r.at]), r.parity, &gave_up))) break;
+        if (!elect_one()) continue;
+        const bool bulk = k < bulk_steps;
+        mbar_expect(bar, w_code + x_code + (bulk ? bulk_bytes : 0u));
+        tma_load_2d(at, &w_map, (int32_t)(k * kMmStageBytes), (int32_t)wr, bar);
+        tma_load_2d(at + w_code, &a_map, (int32_t)(k * kMmStageBytes), (int32_t)m.row0, bar);
+        if (bulk) {
+          const uint32_t sc = at + w_code + x_code;
+          if (w_bulk) bulk_copy(sc, w_from + (size_t)k * block_bytes, block_bytes, bar);
+          if (x_bulk) {
+            bulk_copy(sc + block_bytes, x_from + (size_t)k * block_bytes, block_bytes, bar);
+            if (two)
+              bulk_copy(sc + 2u * block_bytes, x_from + (size_t)c4s * 512u + (size_t)k * block_bytes,
+                        block_bytes, bar);
           }
         }
       }
-      if (!ok)  // let the copies in flight land before the CTA leaves
-        for (int z = 0; z < 1000; ++z) __nanosleep(1000);
     }
+    if (!ok)  // let the copies in flight land before the CTA leaves
+      for (int z = 0; z < 1000; ++z) __nanosleep(1000);
   } else if (warp >= 8) {
     const uint32_t quarter = warp - 8u;
     Ring r;
@@ -457,64 +468,63 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
-    if (lane == 0) {
-      Ring r, acc, sf, sf_last;  // sf_last: the stage that used the scale slot before
-      acc.parity = 1u;
-      uint32_t begun = 0;  // scale slots used so far, up to sf_slots
-      bool ok = true;
-      Ring last;
-      bool any = false;
-      for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const MmTile m = mm_tile(t, first_tile, offs, sh);
-        if (!m.product) continue;
-        if (!(ok = mm_wait(smem_u32(&acc_empty[acc.at]), acc.parity, &gave_up))) break;
-        const uint32_t d = tmem + acc.at * acc_cols;
-        const uint32_t idesc = mm_idesc<MX>((m.tokens + 15u) & ~15u);
-        const bool two = RB == 2 && m.tokens > 128u;
-        uint32_t left = sh.cols;
-        for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages), sf.next(sh.sf_slots)) {
-          // the scale slot's last reader must be done
-          if (begun == sh.sf_slots) {
-            if (!(ok = mm_wait(smem_u32(&empty[sf_last.at]), sf_last.parity, &gave_up))) break;
-            sf_last.next(sh.stages);
-          } else {
-            ++begun;
-          }
-          if (!(ok = mm_wait(smem_u32(&full[r.at]), r.parity, &gave_up))) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          // scales written by cp.async and plain stores: seen by the copy below
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          const uint32_t at = ring + r.at * stage_at;
-          const uint32_t slot = sf_base + sf.at * sf_cols;
-          const u64 sd = scale_desc(at + w_code + x_code);
-#pragma unroll
-          for (uint32_t j = 0; j < ATOMS; ++j) {
-            scales_to_tmem(slot + 4u * j, sd + 32u * j);
-            scales_to_tmem(slot + 4u * ATOMS + 4u * RB * j, sd + 32u * (ATOMS + j));
-            if (two)
-              scales_to_tmem(slot + 4u * ATOMS + 4u * (RB * j + 1u), sd + 32u * (2u * ATOMS + j));
-          }
-          const u64 da = code_desc(at), db = code_desc(at + w_code);
-#pragma unroll
-          for (uint32_t j = 0; j < 4u; ++j) {
-            const uint32_t c = MX ? j / 2u : j;  // piece with this product's scales
-            const uint32_t id = MX ? (j & 1u) * 2u : 0u;
-            if (left > 64u * j)
-              mma_fp4<MX>(d, da + 2u * j, db + 2u * j, idesc | (id << 4) | (id << 29),
-                          slot + 4u * c, slot + 4u * ATOMS + 4u * RB * c, (k | j) != 0u);
-          }
-          left -= 256u;  // wraps only after the last step
-          mma_commit(smem_u32(&empty[r.at]));
-          last = r;
-          any = true;
+    Ring r, acc, sf, sf_last;  // sf_last: the stage that used the scale slot before
+    acc.parity = 1u;
+    uint32_t begun = 0;  // scale slots used so far, up to sf_slots
+    bool ok = true;
+    Ring last;
+    bool any = false;
+    for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const MmTile m = mm_tile(t, first_tile, offs, sh);
+      if (!m.product) continue;
+      if (!(ok = mm_wait(smem_u32(&acc_empty[acc.at]), acc.parity, &gave_up))) break;
+      const uint32_t d = tmem + acc.at * acc_cols;
+      const uint32_t idesc = mm_idesc<MX>((m.tokens + 15u) & ~15u);
+      const bool two = RB == 2 && m.tokens > 128u;
+      uint32_t left = sh.cols;
+      for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages), sf.next(sh.sf_slots)) {
+        // the scale slot's last reader must be done
+        if (begun == sh.sf_slots) {
+          if (!(ok = mm_wait(smem_u32(&empty[sf_last.at]), sf_last.parity, &gave_up))) break;
+          sf_last.next(sh.stages);
+        } else {
+          ++begun;
         }
-        if (!ok) break;
-        mma_commit(smem_u32(&acc_full[acc.at]));
-        acc.next(sh.accs);
+        if (!(ok = mm_wait(smem_u32(&full[r.at]), r.parity, &gave_up))) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        // scales written by cp.async and plain stores: seen by the copy below
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        last = r;
+        any = true;
+        left -= 256u;  // wraps only after the last step
+        if (!elect_one()) continue;
+        const uint32_t at = ring + r.at * stage_at;
+        const uint32_t slot = sf_base + sf.at * sf_cols;
+        const u64 sd = scale_desc(at + w_code + x_code);
+#pragma unroll
+        for (uint32_t j = 0; j < ATOMS; ++j) {
+          scales_to_tmem(slot + 4u * j, sd + 32u * j);
+          scales_to_tmem(slot + 4u * ATOMS + 4u * RB * j, sd + 32u * (ATOMS + j));
+          if (two)
+            scales_to_tmem(slot + 4u * ATOMS + 4u * (RB * j + 1u), sd + 32u * (2u * ATOMS + j));
+        }
+        const u64 da = code_desc(at), db = code_desc(at + w_code);
+#pragma unroll
+        for (uint32_t j = 0; j < 4u; ++j) {
+          const uint32_t c = MX ? j / 2u : j;  // piece with this product's scales
+          const uint32_t id = MX ? (j & 1u) * 2u : 0u;
+          if (left + 256u > 64u * j)
+            mma_fp4<MX>(d, da + 2u * j, db + 2u * j, idesc | (id << 4) | (id << 29),
+                        slot + 4u * c, slot + 4u * ATOMS + 4u * RB * c, (k | j) != 0u);
+        }
+        mma_commit(smem_u32(&empty[r.at]));
       }
-      // the products in flight must end before tensor memory is freed
-      if (any) mm_wait(smem_u32(&empty[last.at]), last.parity, &gave_up);
+      if (!ok) break;
+      if (elect_one()) mma_commit(smem_u32(&acc_full[acc.at]));
+      acc.next(sh.accs);
     }
+    // the products in flight must end before tensor memory is freed
+    if (any) mm_wait(smem_u32(&empty[last.at]), last.parity, &gave_up);
   } else if (warp >= 4) {
     const uint32_t q = warp - 4u;  // this warp's 32 lanes of tensor memory
     uint16_t* mine = turn + q * 32u * 40u;
