@@ -151,13 +151,15 @@ def _p(t: torch.Tensor | None):
         raise TraceError("tensors passed to libtrace_fp4 must be CUDA tensors")
     if not t.is_contiguous():
         raise TraceError("tensors passed to libtrace_fp4 must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
+    if type(stream) is int:
+        return stream
     if stream is None:
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 DEBUG = os.environ.get("TRACE_DEBUG", "0") not in ("", "0")
@@ -749,76 +751,62 @@ class GuidedFakeQuant(torch.autograd.Function):
 # product of captured operands
 # ---------------------------------------------------------------------------
 
-@contextlib.contextmanager
-def _on(stream, *tensors):
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _On:
     """Work on the tensors' own device and on `stream` (default: that
-    device's current stream), so that outputs are allocated there too."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise TraceError(f"tensors on different devices: {dev} and {t.device}")
-    if dev.type != "cuda":
-        raise TraceError("tensors passed to libtrace_fp4 must be CUDA tensors")
-    with torch.cuda.device(dev):
+    device's current stream), so that outputs are allocated there too; gives
+    the stream's handle.  Nothing is switched in the common case, where the
+    device is current and the stream is its own."""
+    __slots__ = ("dev", "stream", "undo")
+
+    def __init__(self, stream, *tensors):
+        dev = tensors[0].device
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise TraceError(f"tensors on different devices: {dev} and {t.device}")
+        if dev.type != "cuda":
+            raise TraceError("tensors passed to libtrace_fp4 must be CUDA tensors")
+        self.dev, self.stream, self.undo = dev, stream, None
+
+    def __enter__(self) -> int:
+        stream, index = self.stream, self.dev.index
+        if stream is None and index == torch.cuda.current_device():
+            return _raw_stream(index)
+        self.undo = contextlib.ExitStack()
+        self.undo.enter_context(torch.cuda.device(self.dev))
         if stream is None:
-            yield torch.cuda.current_stream(dev)
-        else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=dev)
-            with torch.cuda.stream(stream):
-                yield stream
+            return _raw_stream(index)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.dev)
+        self.undo.enter_context(torch.cuda.stream(stream))
+        return stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.undo is not None:
+            self.undo.close()
+        return False
+
+
+def _ptrs(*tensors):
+    """Addresses for the library (0: none); the devices are checked by _On."""
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise TraceError("tensors passed to libtrace_fp4 must be contiguous")
+    return [0 if t is None else t.data_ptr() for t in tensors]
 
 
 def _want(t: torch.Tensor, what: str, dtype, shape=None) -> None:
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise TraceError(f"{what}: unexpected dtype {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise TraceError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def trace_moe_sort_workspace_bytes(tokens: int, k: int, num_experts: int) -> int:
     return int(library().trace_moe_sort_workspace_bytes(tokens, k, num_experts))
-
-
-def trace_moe_sort(expert_ids, id_bytes, tokens, k, num_experts, offsets, rows, slots, workspace,
-                   workspace_bytes, stream=None) -> None:
-    _check(library().trace_moe_sort(_p(expert_ids), id_bytes, tokens, k, num_experts, _p(offsets),
-                                    _p(rows), _p(slots), _p(workspace), workspace_bytes,
-                                    _stream(stream)), "trace_moe_sort")
-
-
-def trace_moe_dispatch(x, tokens, k, cols, rows, slots, y, stream=None) -> None:
-    _check(library().trace_moe_dispatch(_p(x), tokens, k, cols, _p(rows), _p(slots), _p(y),
-                                        _stream(stream)), "trace_moe_dispatch")
-
-
-def trace_moe_combine(y, tokens, k, cols, rows, weights, out, stream=None) -> None:
-    _check(library().trace_moe_combine(_p(y), tokens, k, cols, _p(rows), _p(weights), _p(out),
-                                       _stream(stream)), "trace_moe_combine")
-
-
-def trace_moe_combine_bwd(grad_out, y, tokens, k, cols, rows, slots, weights, grad_y, grad_weights,
-                          stream=None) -> None:
-    _check(library().trace_moe_combine_bwd(_p(grad_out), _p(y), tokens, k, cols, _p(rows),
-                                           _p(slots), _p(weights), _p(grad_y), _p(grad_weights),
-                                           _stream(stream)), "trace_moe_combine_bwd")
-
-
-def trace_fp4_matmul(a_codes, a_scales, a_gscale, rows, cols, num_groups, offsets, a_scale_layout,
-                     w_codes, w_scales, w_gscale, n, num_matrices, w_scale_layout, out,
-                     stream=None) -> None:
-    _check(library().trace_fp4_matmul(_p(a_codes), _p(a_scales), _p(a_gscale), rows, cols,
-                                      num_groups, _p(offsets), a_scale_layout, _p(w_codes),
-                                      _p(w_scales), _p(w_gscale), n, num_matrices, w_scale_layout,
-                                      _p(out), _stream(stream)), "trace_fp4_matmul")
-
-
-def trace_mx_matmul(a_codes, a_scales, rows, cols, num_groups, offsets, a_scale_layout, w_codes,
-                    w_scales, n, num_matrices, w_scale_layout, out, stream=None) -> None:
-    _check(library().trace_mx_matmul(_p(a_codes), _p(a_scales), rows, cols, num_groups,
-                                     _p(offsets), a_scale_layout, _p(w_codes), _p(w_scales), n,
-                                     num_matrices, w_scale_layout, _p(out), _stream(stream)),
-           "trace_mx_matmul")
 
 
 @dataclasses.dataclass
@@ -838,32 +826,44 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, out: MoeRoute | None = 
     if expert_ids.dim() != 2 or expert_ids.shape[1] < 1:
         raise TraceError("expert ids must be [tokens, k]")
     _want(expert_ids, "expert ids", (torch.int32, torch.int64))
-    tokens, k = (int(v) for v in expert_ids.shape)
-    nbytes = trace_moe_sort_workspace_bytes(tokens, k, num_experts)
+    tokens, k = expert_ids.shape
+    lib, base = library(), None
+    nbytes = lib.trace_moe_sort_workspace_bytes(tokens, k, num_experts)
     if nbytes == 0:
         raise TraceError(f"moe_sort: {num_experts} experts for [{tokens}, {k}] ids")
-    dev = expert_ids.device
-    with _on(stream, expert_ids, workspace) as s:
+    with _On(stream, expert_ids, workspace) as s:
         if out is None:
-            out = MoeRoute(torch.empty(num_experts + 2, dtype=torch.int64, device=dev),
-                           torch.empty(tokens, k, dtype=torch.int32, device=dev),
-                           torch.empty(tokens * k, dtype=torch.int32, device=dev))
-        _want(out.offsets, "offsets", torch.int64, (num_experts + 2,))
-        _want(out.rows, "rows", torch.int32, (tokens, k))
-        _want(out.slots, "slots", torch.int32, (tokens * k,))
-        if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        trace_moe_sort(expert_ids, expert_ids.element_size(), tokens, k, num_experts, out.offsets,
-                       out.rows, out.slots, workspace, workspace.numel() * workspace.element_size(),
-                       s)
+            # one allocation: workspace, offsets, rows, slots (the workspace a
+            # multiple of 256 bytes, so each part is aligned)
+            own = 0 if workspace is not None else nbytes // 8
+            at, slots = own + num_experts + 2, tokens * k
+            base = expert_ids.new_empty(at + slots, dtype=torch.int64)
+            words = base.view(torch.int32)
+            out = MoeRoute(torch.as_strided(base, (num_experts + 2,), (1,), own),
+                           torch.as_strided(words, (tokens, k), (k, 1), 2 * at),
+                           torch.as_strided(words, (slots,), (1,), 2 * at + slots))
+            if workspace is None:
+                workspace = base
+        else:
+            _want(out.offsets, "offsets", torch.int64, (num_experts + 2,))
+            _want(out.rows, "rows", torch.int32, (tokens, k))
+            _want(out.slots, "slots", torch.int32, (tokens * k,))
+            _On(None, expert_ids, out.offsets, out.rows, out.slots)
+            if workspace is None:
+                workspace = expert_ids.new_empty(nbytes, dtype=torch.uint8)
+        ids, offsets, rows, slots, ws = _ptrs(expert_ids, out.offsets, out.rows, out.slots, workspace)
+        st = lib.trace_moe_sort(ids, expert_ids.element_size(), tokens, k, num_experts, offsets, rows,
+                                slots, ws, nbytes if workspace is base else
+                                workspace.numel() * workspace.element_size(), s)
+        _check(st, "trace_moe_sort")
     return out
 
 
 def _route_of(route: MoeRoute) -> tuple[int, int]:
-    if route.rows.dim() != 2:
-        raise TraceError("route rows must be [tokens, k]")
-    tokens, k = (int(v) for v in route.rows.shape)
-    _want(route.rows, "route rows", torch.int32)
+    rows = route.rows
+    if rows.dim() != 2 or rows.dtype is not torch.int32:
+        raise TraceError("route rows must be int32 [tokens, k]")
+    tokens, k = rows.shape
     _want(route.slots, "route slots", torch.int32, (tokens * k,))
     return tokens, k
 
@@ -874,12 +874,16 @@ def moe_dispatch_fwd(x: torch.Tensor, route: MoeRoute, out: torch.Tensor | None 
     rows of the dropped group are zero."""
     rows, cols = _bf16_2d(x)
     tokens, k = _route_of(route)
-    _want(x, "tokens", torch.bfloat16, (tokens, cols))
-    with _on(stream, x, route.rows, route.slots, out) as s:
+    if rows != tokens:
+        raise TraceError(f"{rows} tokens, and a route of {tokens}")
+    with _On(stream, x, route.rows, route.slots, out) as s:
         if out is None:
-            out = torch.empty(tokens * k, cols, dtype=torch.bfloat16, device=x.device)
-        _want(out, "out", torch.bfloat16, (tokens * k, cols))
-        trace_moe_dispatch(x, tokens, k, cols, route.rows, route.slots, out, s)
+            out = x.new_empty((tokens * k, cols))
+        else:
+            _want(out, "out", torch.bfloat16, (tokens * k, cols))
+        px, rows, slots, po = _ptrs(x, route.rows, route.slots, out)
+        _check(library().trace_moe_dispatch(px, tokens, k, cols, rows, slots, po, s),
+               "trace_moe_dispatch")
     return out
 
 
@@ -898,11 +902,14 @@ def moe_combine_fwd(y: torch.Tensor, route: MoeRoute, weights: torch.Tensor | No
     _want(y, "expert rows", torch.bfloat16, (tokens * k, cols))
     if weights is not None:
         _want(weights, "weights", torch.float32, (tokens, k))
-    with _on(stream, y, route.rows, weights, out) as s:
+    with _On(stream, y, route.rows, weights, out) as s:
         if out is None:
-            out = torch.empty(tokens, cols, dtype=torch.bfloat16, device=y.device)
-        _want(out, "out", torch.bfloat16, (tokens, cols))
-        trace_moe_combine(y, tokens, k, cols, route.rows, weights, out, s)
+            out = y.new_empty((tokens, cols))
+        else:
+            _want(out, "out", torch.bfloat16, (tokens, cols))
+        py, rows, w, po = _ptrs(y, route.rows, weights, out)
+        _check(library().trace_moe_combine(py, tokens, k, cols, rows, w, po, s),
+               "trace_moe_combine")
     return out
 
 
@@ -914,11 +921,13 @@ def moe_combine_bwd(grad: torch.Tensor, y: torch.Tensor, route: MoeRoute, weight
     _want(y, "expert rows", torch.bfloat16, (tokens * k, cols))
     _want(grad, "gradient", torch.bfloat16, (tokens, cols))
     _want(weights, "weights", torch.float32, (tokens, k))
-    with _on(stream, grad, y, route.rows, route.slots, weights) as s:
+    with _On(stream, grad, y, route.rows, route.slots, weights) as s:
         grad_y = torch.empty_like(y)
-        grad_w = torch.empty(tokens, k, dtype=torch.float32, device=y.device)
-        trace_moe_combine_bwd(grad, y, tokens, k, cols, route.rows, route.slots, weights, grad_y,
-                              grad_w, s)
+        grad_w = torch.empty_like(weights)
+        pg, py, rows, slots, w, gy, gw = _ptrs(grad, y, route.rows, route.slots, weights, grad_y,
+                                               grad_w)
+        _check(library().trace_moe_combine_bwd(pg, py, tokens, k, cols, rows, slots, w, gy, gw, s),
+               "trace_moe_combine_bwd")
     return grad_y, grad_w
 
 
@@ -965,43 +974,56 @@ def moe_combine(y: torch.Tensor, route: MoeRoute, weights: torch.Tensor) -> torc
     return moe_combine_fwd(y, route, weights)
 
 
-def _matmul_operand(cap, cols: int | None, what: str) -> tuple[int, int, int]:
-    """(rows, cols, scale layout) of a captured FP4 operand: row-major scales
-    are 2-D and tell cols; tiled ones are flat and need it."""
-    _want(cap.codes, f"{what} codes", torch.uint8)
-    _want(cap.scales, f"{what} scales", torch.uint8)
-    bs = 16 if isinstance(cap, Capture) else 32
-    layout = TRACE_SCALES_ROW_MAJOR if cap.scales.dim() == 2 else TRACE_SCALES_TILED_128x4
+def _matmul_operand(cap, cols: int, bs: int, what: str) -> tuple[int, int]:
+    """(rows, scale layout) of a captured FP4 operand: row-major scales are
+    2-D, tiled ones flat."""
+    codes, scales = cap.codes, cap.scales
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+        raise TraceError(f"{what}: codes and scales must be uint8")
+    rows, odd = divmod(codes.numel() * 2, cols)
+    if odd:
+        raise TraceError(f"{what}: {codes.numel()} bytes of codes are no rows of {cols}")
+    c = cols // bs
+    if scales.dim() == 2:
+        layout, want = TRACE_SCALES_ROW_MAJOR, rows * c
+    else:
+        layout, want = TRACE_SCALES_TILED_128x4, -(-rows // 128) * -(-c // 4) * 512
+    if scales.numel() != want:
+        raise TraceError(f"{what}: {scales.numel()} scales for [{rows}, {cols}]")
+    return rows, layout
+
+
+def _matmul(a, w, cols, offsets, matrices, out, stream, bs):
     if cols is None:
-        if layout != TRACE_SCALES_ROW_MAJOR:
-            raise TraceError(f"{what}: cols is needed with tiled scales")
-        cols = int(cap.scales.shape[1]) * bs
-    if cols <= 0 or cols % 32 or cap.codes.numel() * 2 % cols:
-        raise TraceError(f"{what}: {cap.codes.numel()} bytes of codes are no rows of {cols}")
-    rows = cap.codes.numel() * 2 // cols
-    if cap.scales.numel() != trace_scale_bytes(rows, cols, bs, layout):
-        raise TraceError(f"{what}: {cap.scales.numel()} scales for [{rows}, {cols}]")
-    return rows, cols, layout
-
-
-def _matmul(a, w, cols, offsets, groups, matrices, out, stream, fmt):
-    rows, cols, la = _matmul_operand(a, cols, "a")
-    wrows, _, lw = _matmul_operand(w, cols, "w")
+        s = next((c.scales for c in (a, w) if c.scales.dim() == 2), None)
+        if s is None:
+            raise TraceError("cols is needed when both scales are tiled")
+        cols = s.shape[1] * bs
+    if cols <= 0 or cols % 32:
+        raise TraceError(f"cols must be a multiple of 32: {cols}")
+    rows, la = _matmul_operand(a, cols, bs, "a")
+    wrows, lw = _matmul_operand(w, cols, bs, "w")
+    groups = _groups(offsets, rows)
     if matrices < 1 or wrows % matrices or wrows == 0:
         raise TraceError(f"w: {wrows} rows are no {matrices} matrices")
     n = wrows // matrices
-    with _on(stream, a.codes, a.scales, w.codes, w.scales, offsets, out) as s:
+    ga, gw = (a.gscale, w.gscale) if bs == 16 else (None, None)
+    with _On(stream, a.codes, a.scales, w.codes, w.scales, offsets, ga, gw, out) as s:
         if out is None:
-            out = torch.empty(rows, n, dtype=torch.bfloat16, device=a.codes.device)
-        _want(out, "out", torch.bfloat16, (rows, n))
-        if fmt == "nvfp4":
-            _want(a.gscale, "a global scales", torch.float32, (groups,))
-            _want(w.gscale, "w global scales", torch.float32, (matrices,))
-            trace_fp4_matmul(a.codes, a.scales, a.gscale, rows, cols, groups, offsets, la, w.codes,
-                             w.scales, w.gscale, n, matrices, lw, out, s)
+            out = a.codes.new_empty((rows, n), dtype=torch.bfloat16)
         else:
-            trace_mx_matmul(a.codes, a.scales, rows, cols, groups, offsets, la, w.codes, w.scales,
-                            n, matrices, lw, out, s)
+            _want(out, "out", torch.bfloat16, (rows, n))
+        ac, asc, wc, wsc, po, pf = _ptrs(a.codes, a.scales, w.codes, w.scales, out, offsets)
+        if bs == 16:
+            _want(ga, "a global scales", torch.float32, (groups,))
+            _want(gw, "w global scales", torch.float32, (matrices,))
+            pa, pw = _ptrs(ga, gw)
+            st = library().trace_fp4_matmul(ac, asc, pa, rows, cols, groups, pf, la, wc, wsc, pw, n,
+                                            matrices, lw, po, s)
+        else:
+            st = library().trace_mx_matmul(ac, asc, rows, cols, groups, pf, la, wc, wsc, n, matrices,
+                                           lw, po, s)
+        _check(st, "trace_fp4_matmul" if bs == 16 else "trace_mx_matmul")
     return out
 
 
@@ -1015,11 +1037,7 @@ def fp4_matmul(a: Capture, w: Capture, cols: int | None = None, out: torch.Tenso
     training side differentiates through trace_fake_quant."""
     if not isinstance(a, Capture) or not isinstance(w, Capture):
         raise TraceError("fp4_matmul takes two NVFP4 captures")
-    if cols is None and a.scales.dim() != 2 and w.scales.dim() == 2:
-        cols = int(w.scales.shape[1]) * 16
-    rows = None if cols is None else a.codes.numel() * 2 // cols
-    return _matmul(a, w, cols, a.offsets, _groups(a.offsets, rows), int(w.gscale.numel()), out,
-                   stream, "nvfp4")
+    return _matmul(a, w, cols, a.offsets, w.gscale.numel(), out, stream, 16)
 
 
 def mx_matmul(a: MxCapture, w: MxCapture, cols: int | None = None,
@@ -1029,10 +1047,7 @@ def mx_matmul(a: MxCapture, w: MxCapture, cols: int | None = None,
     (int64 row bounds of a) and `groups` (matrices stacked in w) are given."""
     if not isinstance(a, MxCapture) or not isinstance(w, MxCapture):
         raise TraceError("mx_matmul takes two MXFP4 captures")
-    if cols is None and a.scales.dim() != 2 and w.scales.dim() == 2:
-        cols = int(w.scales.shape[1]) * 32
-    rows = None if cols is None else a.codes.numel() * 2 // cols
-    return _matmul(a, w, cols, offsets, _groups(offsets, rows), groups, out, stream, "mxfp4")
+    return _matmul(a, w, cols, offsets, groups, out, stream, 32)
 
 
 def matmul_status(stream=None) -> bool:
