@@ -14,38 +14,41 @@
 // column j, tensor-memory column = token.
 //
 // One persistent CTA per SM walks tiles; its warps are specialised:
-//   warp 0     copies both operands' codes by TMA, 256 k-elements (128 bytes
+//   warp 0      copies both operands' codes by TMA, 256 k-elements (128 bytes
 //              per row, 128-byte swizzle) per stage of a shared-memory ring,
 //              and tiled scales whose 128-row block is the tile's own;
-//   warps 8-11 copy all other scales into the ring in the 128 x 4 tiled order
+//   warps 12-15 copy all other scales into the ring in the 128 x 4 tiled order
 //              the tensor core wants, from either layout and at any row (a
 //              group starts anywhere), and zero what lies past the last k;
-//   warp 1     moves a stage's scales to tensor memory and issues its
+//   warp 1      moves a stage's scales to tensor memory and issues its
 //              products;
-//   warps 4-7  read finished accumulators and write bf16 rows of out, while
+//   warps 4-11 read finished accumulators and write bf16 rows of out, while
 //              the next tile runs on the other accumulator.
 // Each role is one warp that runs alone on its scheduler, so a stage costs it
 // its instructions' latencies: ring positions are counters and not quotients,
 // and the loops over a stage's parts are unrolled.
 #pragma once
 
-constexpr int kMmThreads = 384;
+constexpr int kMmThreads = 512;
 constexpr int kMmM = 128;            // w rows of a tile
 constexpr int kMmStageBytes = 128;   // code bytes per row and stage: 256 elements
 constexpr int kMmMaxStages = 8;
+constexpr uint32_t kMmTurnBytes = 12 * 16 * 40 * 2;  // output pieces being transposed
+constexpr uint32_t kMmTokens = 192, kMmPairTokens = 256;  // of the largest tiles
 constexpr uint32_t kMmTmemCols = 512;
 // Polls of one wait before a CTA gives up (each try_wait itself suspends):
 // a guard, every wait ends as its copies and products do.
-constexpr uint32_t kMmPolls = 1u << 22;
+constexpr uint32_t kMmPolls = 1u << 20;
 
 struct MmShape {
   int64_t rows, n;
   uint32_t cols, scols;        // k-elements, scale columns
   int32_t groups, matrices;
   uint32_t nt;                 // tokens of a full tile (multiple of 16)
-  uint32_t n_tiles;            // ceil(n / 128)
+  uint32_t n_tiles;            // ceil(n / 128), of pairs ceil(n / 256)
   uint32_t ksteps;             // stages of a whole product
   uint32_t stages, accs, sf_slots;
+  uint32_t split;              // CTAs of a cluster that share one tile's k (1: none)
   uint8_t a_tiled, w_tiled;
   uint8_t a_bytes, w_bytes;    // row-major scales that are not 4-byte words
   uint8_t out16;               // rows of out are 16-byte aligned
@@ -58,16 +61,21 @@ __device__ uint32_t g_matmul_gave_up;  // set if a wait ran out of polls
 // (a small activation against a large weight).  |sum| is 0 or in
 // [2^-20, 2^54], so with the exponents halved no step over- or underflows
 // unless the result does; past +-250 the result is 0 or infinite anyway.
+// Exponents within +-60 leave nothing to lose: one factor then, the same bits.
 struct OutScale {
   float m, p, q;
-  __device__ __forceinline__ float apply(float sum) const { return ((sum * m) * p) * q; }
+  bool one;  // p and q are 1
+  __device__ __forceinline__ float apply(float sum) const {
+    return one ? sum * m : ((sum * m) * p) * q;
+  }
 };
 
 __device__ __forceinline__ OutScale make_out_scale(float ga, float gw) {
   const double d = (double)ga * (double)gw;  // exact
-  OutScale s{(float)d, 1.0f, 1.0f};
+  OutScale s{(float)d, 1.0f, 1.0f, true};
   int e = ((__double2hiint(d) >> 20) & 0x7FF) - 1023;
-  if (e == -1023 || e == 1024) return s;  // zero or not finite
+  if (e == -1023 || e == 1024 || (e >= -60 && e <= 60)) return s;  // zero or not finite, or plain
+  s.one = false;
   s.m = (float)__hiloint2double((__double2hiint(d) & 0x000FFFFF) | (1023 << 20), __double2loint(d));
   e = max(-252, min(e, 250));
   s.p = __int_as_float((e / 2 + 127) << 23);
@@ -89,6 +97,33 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
                : "memory");
 }
 
+// The same shared-memory address in another CTA of the cluster.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// Only what tcgen05 instructions read or wrote hangs on this arrival (a
+// cluster-scope release would order memory that nobody shares, and cost more
+// than a stage's products).
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ float ld_peer(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+// Every thread of every CTA of the cluster, with its earlier writes seen.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // One lane of a converged warp; ptxas knows that a branch on it leaves a
 // single thread and keeps the operands of what it issues in uniform registers.
 __device__ __forceinline__ bool elect_one() {
@@ -98,27 +133,54 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0u;
 }
 
-// Bounded wait for a phase; false once any wait of the CTA has given up.
-// The lanes of a warp agree on the answer.
+// A value that every lane of a warp holds: from here on in uniform registers,
+// which what the tensor core and the copy engine are given has to be in (a
+// stage's 12 scale copies and 4 products issue in 250 cycles instead of 350).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+// Up to 256 polls for a phase to end.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 c;\n\tmov.u32 c, 256;\n\t"
+      "again:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra over;\n\tsub.u32 c, c, 1;\n\tsetp.ne.u32 q, c, 0;\n\t@q bra again;\n\t"
+      "over:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+
+// Bounded wait of a warp for a phase (lanes may name different barriers);
+// false once any wait of the CTA has given up.  60 cycles where the phase has
+// ended, against 90 of a loop over single polls.
 __device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
-  bool ok = false;
-  for (uint32_t i = 0; i < kMmPolls; ++i) {
-    if ((ok = mbar_try_wait(bar, parity))) break;
-    if ((i & 255u) == 255u && *gave_up) break;
+  for (uint32_t i = 0; i < kMmPolls / 256u; ++i) {
+    if (__all_sync(0xFFFFFFFFu, mbar_poll(bar, parity))) return true;
+    if (__any_sync(0xFFFFFFFFu, *gave_up != 0u)) break;
   }
-  if (__all_sync(0xFFFFFFFFu, ok)) return true;
   *gave_up = 1u;
   g_matmul_gave_up = 1u;
   return false;
 }
 
+// CG 2: `bar` may lie in the other CTA of the pair.
+template <int CG>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t x,
                                             int32_t y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 
 // A contiguous copy, counted on the stage's barrier (whose expected bytes
@@ -149,56 +211,94 @@ __device__ __forceinline__ u64 scale_desc(uint32_t smem) {
   return (u64)((smem & 0x3FFFFu) >> 4) | ((u64)(128 >> 4) << 32) | ((u64)1 << 46);
 }
 
-// Instruction descriptor: E2M1 x E2M1, K-major, M = 128, N = n; the scale
-// type and which bytes of the scale words the instruction uses (ids).
-template <bool MX>
+// Instruction descriptor: E2M1 x E2M1, K-major, M = 128 per CTA, N = n; the
+// scale type (the ids of the bytes used in a scale word are added later).
+template <bool MX, int CG>
 __device__ __forceinline__ uint32_t mm_idesc(uint32_t n) {
-  return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (MX ? 1u << 23 : 0u) | ((128u >> 4) << 24);
+  return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (MX ? 1u << 23 : 0u) |
+         ((CG * 128u >> 4) << 24);
 }
 
-template <bool MX>
+// Columns of a product of `tokens` tokens: whole 16s in each CTA's share.
+template <int CG>
+__device__ __forceinline__ uint32_t mm_width(uint32_t tokens) {
+  return (tokens + 16u * CG - 1u) / (16u * CG) * (16u * CG);
+}
+
+// D += A B on one CTA's tensor core or (CG 2) on a pair's: each CTA then
+// holds its 128 rows of A, half the rows of B, and its rows of D.
+#define TRACE_MMA_FP4(GROUP, KIND, VEC)                                                   \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"                        \
+               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND ".block_scale.scale_vec::" VEC \
+               " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                         \
+               "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)            \
+               : "memory")
+template <bool MX, int CG>
 __device__ __forceinline__ void mma_fp4(uint32_t d, u64 a, u64 b, uint32_t idesc, uint32_t sa,
                                         uint32_t sb, bool add) {
-  if (MX)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-        : "memory");
+  if (MX && CG == 1) TRACE_MMA_FP4("1", "mxf4", "2X");
+  if (MX && CG == 2) TRACE_MMA_FP4("2", "mxf4", "2X");
+  if (!MX && CG == 1) TRACE_MMA_FP4("1", "mxf4nvf4", "4X");
+  if (!MX && CG == 2) TRACE_MMA_FP4("2", "mxf4nvf4", "4X");
 }
+#undef TRACE_MMA_FP4
 
+// 512 bytes of scales to 4 columns of tensor memory (CG 2: each CTA of the
+// pair its own).
+template <int CG>
 __device__ __forceinline__ void scales_to_tmem(uint32_t tmem, u64 desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-               : "memory");
+  if (CG == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
 }
 
 // The barrier's phase ends when every product and copy issued so far by this
-// thread has.
+// thread has (CG 2: the barrier at this address in both CTAs).
+template <int CG>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
+  if (CG == 1)
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15])
-      : "r"(addr));
+// 32 lanes x 16 columns of an accumulator: lane / 4 (+ 8, 16, 24) are the rows
+// and 2 (lane % 4) (+ 8), and the next, the columns: v[0..1] row + 0, v[2..3]
+// row + 8, v[4..7] the same of the columns + 8, v[8..15] the rows + 16.
+__device__ __forceinline__ void tmem_ld_32x16(uint32_t addr, uint32_t* v) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(v[8 * h]), "=r"(v[8 * h + 1]), "=r"(v[8 * h + 2]), "=r"(v[8 * h + 3]),
+          "=r"(v[8 * h + 4]), "=r"(v[8 * h + 5]), "=r"(v[8 * h + 6]), "=r"(v[8 * h + 7])
+        : "r"(addr + ((uint32_t)h << 20)));
 }
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// Four 8 x 8 tiles of 16-bit words, stored transposed; each lane gives the
+// address of one 16-byte row.
+__device__ __forceinline__ void st_matrix_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Every load so far has arrived; the words pass through, so that no use of
+// them moves in front of the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
 }
 
 // A position in a ring of `size` slots and the parity of its current round.
@@ -221,7 +321,8 @@ struct Ring {
 struct MmTile {
   int32_t group;
   int64_t row0;       // first token row
-  uint32_t tokens;    // rows of this tile that belong to the group
+  uint32_t lead;      // rows in front that belong to earlier groups
+  uint32_t tokens;    // rows up to the group's last in this tile
   uint32_t j0;        // first output column
   bool product;       // false: a group without a matrix, its rows are zero
 };
@@ -232,6 +333,15 @@ __device__ __forceinline__ int64_t mm_bound(const int64_t* offs, int32_t g, cons
   return v < 0 ? 0 : (v > sh.rows ? sh.rows : v);
 }
 
+// The row that a group's tiles are counted from: a pair's lie at multiples of
+// 128 (and the first begins at a multiple of 64), so that the copy engine can
+// take tiled scales as they are, at most two blocks for a tile.
+template <int CG>
+__device__ __forceinline__ int64_t mm_start(int64_t bound) {
+  return CG == 2 ? bound & ~(int64_t)127 : bound;
+}
+
+template <int CG>
 __device__ __forceinline__ MmTile mm_tile(uint32_t t, const uint32_t* first_tile,
                                           const int64_t* offs, const MmShape& sh) {
   MmTile m;
@@ -242,15 +352,19 @@ __device__ __forceinline__ MmTile mm_tile(uint32_t t, const uint32_t* first_tile
     if (first_tile[mid] <= tt) lo = mid; else hi = mid - 1;
   }
   m.group = lo;
-  m.row0 = mm_bound(offs, lo, sh) + (int64_t)(tt - first_tile[lo]) * sh.nt;
-  const int64_t left = mm_bound(offs, lo + 1, sh) - m.row0;
-  m.tokens = left < (int64_t)sh.nt ? (uint32_t)left : sh.nt;
-  m.j0 = (t - tt * sh.n_tiles) * kMmM;
+  const int64_t begin = mm_bound(offs, lo, sh);
+  const int64_t from = mm_start<CG>(begin) + (int64_t)(tt - first_tile[lo]) * sh.nt;
+  m.row0 = CG == 2 && begin - from >= 64 ? from + 64 : from;
+  m.lead = begin > m.row0 ? (uint32_t)(begin - m.row0) : 0u;
+  const int64_t end = mm_bound(offs, lo + 1, sh);
+  m.tokens = (uint32_t)((end < from + sh.nt ? end : from + sh.nt) - m.row0);
+  m.j0 = (t - tt * sh.n_tiles) * (CG * kMmM);
   m.product = lo < sh.matrices;
   return m;
 }
 
 // first_tile[0 .. groups] by a scan over the CTA.
+template <int CG>
 __device__ __forceinline__ void mm_table(uint32_t* first_tile, uint32_t* warp_sum,
                                          const int64_t* offs, const MmShape& sh) {
   const uint32_t lane = threadIdx.x % 32u, warp = threadIdx.x / 32u;
@@ -259,8 +373,8 @@ __device__ __forceinline__ void mm_table(uint32_t* first_tile, uint32_t* warp_su
     const int32_t g = g0 + (int32_t)threadIdx.x;
     uint32_t tiles = 0u;
     if (g < sh.groups) {
-      const int64_t cnt = mm_bound(offs, g + 1, sh) - mm_bound(offs, g, sh);
-      if (cnt > 0) tiles = (uint32_t)((cnt + sh.nt - 1) / sh.nt);
+      const int64_t begin = mm_bound(offs, g, sh), end = mm_bound(offs, g + 1, sh);
+      if (end > begin) tiles = (uint32_t)((end - mm_start<CG>(begin) + sh.nt - 1) / sh.nt);
     }
     uint32_t sum = tiles;
 #pragma unroll
@@ -344,82 +458,136 @@ __device__ __forceinline__ void copy_scales(const ScaleSrc& s, const uint8_t* ba
 }
 
 // ---------------------------------------------------------------------------
-// The kernel; RB: 128-row blocks of token scales (1 up to 128 tokens, else 2)
+// The kernel.  RB: 128-row blocks of token scales (1 up to 128 tokens, else
+// 2).  CG: CTAs that share a tile.  With CG 2 a pair holds 256 rows of w and
+// the same tokens: each CTA copies its own 128 rows of w, half of the tokens'
+// codes and all of their scales, every part by TMA and counted on the leader's
+// barrier, and the leader's warp 1 issues for both.
 // ---------------------------------------------------------------------------
-template <bool MX, int RB>
+struct MmMaps {
+  CUtensorMap a, w;    // codes
+  CUtensorMap as, ws;  // CG 2: tiled scales, a row per 128-row block
+};
+
+template <bool MX, int RB, int CG>
 __global__ void __launch_bounds__(kMmThreads, 1)
-    k_matmul(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap w_map,
-             const uint8_t* __restrict__ as, const uint8_t* __restrict__ ws,
-             const float* __restrict__ ag, const float* __restrict__ wg,
-             const int64_t* __restrict__ offs, MmShape sh, uint16_t* __restrict__ out) {
+    k_matmul(const __grid_constant__ MmMaps maps, const uint8_t* __restrict__ as,
+             const uint8_t* __restrict__ ws, const float* __restrict__ ag,
+             const float* __restrict__ wg, const int64_t* __restrict__ offs, MmShape sh,
+             uint16_t* __restrict__ out) {
   constexpr uint32_t ATOMS = MX ? 2 : 4;  // groups of 4 scale columns per stage
   constexpr uint32_t w_code = kMmM * kMmStageBytes;
   constexpr uint32_t block_bytes = ATOMS * 512u;  // a block's scales per stage
+  constexpr bool PAIR = CG == 2;
+  constexpr uint32_t OUT = PAIR ? 3u : 2u;  // warps that write out, per quarter of a tile's rows
+  constexpr uint32_t PIECES = ((PAIR ? kMmPairTokens : kMmTokens) / 16u + OUT - 1u) / OUT;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) u64 full[kMmMaxStages], empty[kMmMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base_s, warp_sum[kMmThreads / 32];
   __shared__ volatile uint32_t gave_up;
   const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32u, 0), lane = threadIdx.x % 32u;
-  const uint32_t x_code = sh.nt * kMmStageBytes;
+  const uint32_t x_code = sh.nt / CG * kMmStageBytes;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t stage_at = (w_code + x_code + block_bytes * (1u + RB) + 1023u) & ~1023u;
-  uint8_t* after = smem_raw + (ring - smem_u32(smem_raw)) + sh.stages * stage_at;
-  uint16_t* turn = reinterpret_cast<uint16_t*>(after);               // [4][32][40] bf16
-  uint32_t* first_tile = reinterpret_cast<uint32_t*>(after + 4 * 32 * 40 * 2);
+  uint8_t* ring_p = smem_raw + (ring - smem_u32(smem_raw));
+  uint8_t* after = ring_p + sh.stages * stage_at;  // 12 warps x 16 tokens x 40 bf16, the table
+  uint32_t* first_tile = reinterpret_cast<uint32_t*>(after + kMmTurnBytes);
+  const uint32_t rank = cluster_rank();  // in a pair, or among the CTAs of a split
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < sh.stages; ++s) {
-      mbar_init(smem_u32(&full[s]), 1 + 128);  // the TMA thread and the scale lanes
+      // the TMA thread, and the scale lanes
+      mbar_init(smem_u32(&full[s]), PAIR ? 1 : 1 + 128);
       mbar_init(smem_u32(&empty[s]), 1);
     }
     for (uint32_t a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&acc_full[a]), 1);
-      mbar_init(smem_u32(&acc_empty[a]), 4);
+      mbar_init(smem_u32(&acc_empty[a]), 4 * OUT * CG);
     }
     gave_up = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_begin();
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&tmem_base_s)),
-                 "r"(kMmTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&tmem_base_s)),
+                   "r"(kMmTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&tmem_base_s)),
+                   "r"(kMmTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
-  mm_table(first_tile, warp_sum, offs, sh);
+  mm_table<CG>(first_tile, warp_sum, offs, sh);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if (PAIR) cluster_sync();  // the other CTA's barriers exist
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = tmem_base_s;
+  const uint32_t tmem = uniform(tmem_base_s);
   const uint32_t tiles = first_tile[sh.groups] * sh.n_tiles;
   const uint32_t acc_cols = (sh.nt + 31u) & ~31u;
   constexpr uint32_t sf_cols = 4u * ATOMS * (1u + RB);  // tensor-memory columns of a stage's scales
   const uint32_t sf_base = tmem + sh.accs * acc_cols;
+  // this CTA's tiles, and its part of k
+  const uint32_t team = PAIR ? 2u : sh.split;
+  const uint32_t t0 = blockIdx.x / team, t_step = gridDim.x / team;
+  const uint32_t k_rank = PAIR ? 0u : rank;
+  const uint32_t k0 = k_rank * sh.ksteps / sh.split, k1 = (k_rank + 1u) * sh.ksteps / sh.split;
+  const uint32_t j_rank = PAIR ? rank * kMmM : 0u;
 
   if (warp == 0) {
     Ring r;
     r.parity = 1u;  // the first round finds every slot empty
     bool ok = true;
     const uint32_t c4s = (sh.scols + 3u) / 4u, bulk_steps = sh.scols / (4u * ATOMS);
-    for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const MmTile m = mm_tile(t, first_tile, offs, sh);
+    for (uint32_t t = t0; ok && t < tiles; t += t_step) {
+      const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       if (!m.product) continue;
-      const int64_t wr = m.group * sh.n + m.j0;
-      const bool w_bulk = scales_bulk(sh.w_tiled, wr), x_bulk = scales_bulk(sh.a_tiled, m.row0);
+      const int64_t wr = m.group * sh.n + m.j0 + j_rank;
+      const int32_t w_row = (int32_t)uniform((uint32_t)wr);
+      if (PAIR) {
+        // blocks of 128 rows that the tile's scales lie in
+        const uint32_t width = mm_width<CG>(m.tokens);
+        const bool two = (uint32_t)(m.row0 % 128) + width > 128u;
+        const int32_t wb = w_row / 128, row = (int32_t)uniform((uint32_t)m.row0), xb = row / 128;
+        const int32_t xr = row + (int32_t)uniform(rank * (width / 2u));
+        const uint32_t bytes = 2u * (w_code + x_code + (two ? 3u : 2u) * block_bytes);
+        for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages)) {
+          const uint32_t at = uniform(ring + r.at * stage_at), sc = at + w_code + x_code;
+          const uint32_t own = smem_u32(&full[r.at]), bar = peer_smem(own, 0);
+          if (!(ok = mm_wait(smem_u32(&empty[r.at]), r.parity, &gave_up))) break;
+          if (!elect_one()) continue;
+          if (rank == 0) mbar_expect(own, bytes);
+          tma_load_2d<CG>(at, &maps.w, (int32_t)(k * kMmStageBytes), w_row, bar);
+          tma_load_2d<CG>(at + w_code, &maps.a, (int32_t)(k * kMmStageBytes), xr, bar);
+          tma_load_2d<CG>(sc, &maps.ws, (int32_t)(k * ATOMS * 64u), wb, bar);
+          tma_load_2d<CG>(sc + block_bytes, &maps.as, (int32_t)(k * ATOMS * 64u), xb, bar);
+          if (two)
+            tma_load_2d<CG>(sc + 2u * block_bytes, &maps.as, (int32_t)(k * ATOMS * 64u), xb + 1,
+                            bar);
+        }
+        continue;
+      }
+      const bool w_bulk = scales_bulk(sh.w_tiled, wr) && wr < sh.n * sh.matrices;
+      const bool x_bulk = scales_bulk(sh.a_tiled, m.row0);
       const bool two = RB == 2 && m.tokens > 128u;
       const uint8_t* w_from = ws + (size_t)(wr / 128) * c4s * 512u;
       const uint8_t* x_from = as + (size_t)(m.row0 / 128) * c4s * 512u;
       const uint32_t bulk_bytes = (w_bulk ? block_bytes : 0u) +
                                   (x_bulk ? (two ? 2u : 1u) * block_bytes : 0u);
-      for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages)) {
-        const uint32_t bar = smem_u32(&full[r.at]), at = ring + r.at * stage_at;
+      for (uint32_t k = k0; k < k1; ++k, r.next(sh.stages)) {
+        const uint32_t bar = smem_u32(&full[r.at]), at = uniform(ring + r.at * stage_at);
         if (!(ok = mm_wait(smem_u32(&empty[r.at]), r.parity, &gave_up))) break;
         if (!elect_one()) continue;
         const bool bulk = k < bulk_steps;
         mbar_expect(bar, w_code + x_code + (bulk ? bulk_bytes : 0u));
-        tma_load_2d(at, &w_map, (int32_t)(k * kMmStageBytes), (int32_t)wr, bar);
-        tma_load_2d(at + w_code, &a_map, (int32_t)(k * kMmStageBytes), (int32_t)m.row0, bar);
+        tma_load_2d<CG>(at, &maps.w, (int32_t)(k * kMmStageBytes), w_row, bar);
+        tma_load_2d<CG>(at + w_code, &maps.a, (int32_t)(k * kMmStageBytes), (int32_t)m.row0, bar);
         if (bulk) {
           const uint32_t sc = at + w_code + x_code;
           if (w_bulk) bulk_copy(sc, w_from + (size_t)k * block_bytes, block_bytes, bar);
@@ -434,15 +602,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     }
     if (!ok)  // let the copies in flight land before the CTA leaves
       for (int z = 0; z < 1000; ++z) __nanosleep(1000);
-  } else if (warp >= 8) {
-    const uint32_t quarter = warp - 8u;
+  } else if (warp >= 12 && !PAIR) {
+    const uint32_t quarter = warp - 12u;
     Ring r;
     r.parity = 1u;
     bool ok = true;
-    for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const MmTile m = mm_tile(t, first_tile, offs, sh);
+    for (uint32_t t = t0; ok && t < tiles; t += t_step) {
+      const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       if (!m.product) continue;
-      const int64_t wr = m.group * sh.n + m.j0;
+      const int64_t wr = m.group * sh.n + m.j0 + j_rank;
       const ScaleSrc sw = scale_src(ws, sh.w_tiled, sh.w_bytes, wr, sh.n * sh.matrices, sh.scols,
                                     quarter, lane);
       const ScaleSrc s0 = scale_src(as, sh.a_tiled, sh.a_bytes, m.row0, sh.rows, sh.scols, quarter,
@@ -451,12 +619,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       const ScaleSrc s1 = scale_src(as, sh.a_tiled, sh.a_bytes, m.row0 + 128, sh.rows, sh.scols,
                                     quarter, lane);
       const uint32_t word = w_code + x_code + 16u * lane + 4u * quarter;
-      for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages)) {
+      for (uint32_t k = k0; k < k1; ++k, r.next(sh.stages)) {
         if (!(ok = mm_wait(smem_u32(&empty[r.at]), r.parity, &gave_up))) break;
         const uint32_t at = ring + r.at * stage_at + word, bar = smem_u32(&full[r.at]);
         copy_scales<ATOMS>(sw, ws, at, 512u, k, sh.scols);
-        copy_scales<ATOMS>(s0, as, at + block_bytes, 512u, k, sh.scols);
-        if (two) copy_scales<ATOMS>(s1, as, at + 2u * block_bytes, 512u, k, sh.scols);
+        // rows past the tile's last token reach no output
+        if (32u * quarter < m.tokens)
+          copy_scales<ATOMS>(s0, as, at + block_bytes, 512u, k, sh.scols);
+        if (two && 128u + 32u * quarter < m.tokens)
+          copy_scales<ATOMS>(s1, as, at + 2u * block_bytes, 512u, k, sh.scols);
         if (sw.bytes || s0.bytes) {  // plain stores: nothing that arrives by itself
           asm volatile("cp.async.wait_all;" ::: "memory");
           mbar_arrive(bar);
@@ -467,122 +638,194 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 1) {
+  } else if (warp == 1 && (!PAIR || rank == 0)) {
     Ring r, acc, sf, sf_last;  // sf_last: the stage that used the scale slot before
     acc.parity = 1u;
     uint32_t begun = 0;  // scale slots used so far, up to sf_slots
-    bool ok = true;
+    bool ok = true, any = false;
     Ring last;
-    bool any = false;
-    for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const MmTile m = mm_tile(t, first_tile, offs, sh);
+    for (uint32_t t = t0; ok && t < tiles; t += t_step) {
+      const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       if (!m.product) continue;
+      const uint32_t width = uniform(mm_width<CG>(m.tokens));
+      const uint32_t d = uniform(tmem + acc.at * acc_cols), idesc = mm_idesc<MX, CG>(width);
+      // tokens that start in the middle of a block: two columns of scales on
+      const uint32_t shift = PAIR ? uniform((uint32_t)(m.row0 % 128) / 32u) : 0u;
+      const bool two = RB == 2 && 32u * shift + width > 128u;
       if (!(ok = mm_wait(smem_u32(&acc_empty[acc.at]), acc.parity, &gave_up))) break;
-      const uint32_t d = tmem + acc.at * acc_cols;
-      const uint32_t idesc = mm_idesc<MX>((m.tokens + 15u) & ~15u);
-      const bool two = RB == 2 && m.tokens > 128u;
-      uint32_t left = sh.cols;
-      for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages), sf.next(sh.sf_slots)) {
-        // the scale slot's last reader must be done
-        if (begun == sh.sf_slots) {
-          if (!(ok = mm_wait(smem_u32(&empty[sf_last.at]), sf_last.parity, &gave_up))) break;
-          sf_last.next(sh.stages);
-        } else {
-          ++begun;
+      for (uint32_t k = k0; k < k1; ++k, r.next(sh.stages), sf.next(sh.sf_slots)) {
+        // The stage is full, and the scale slot's last reader is done: half of
+        // the lanes wait for each (with a slot for every stage the first says
+        // the second).
+        uint32_t bar = smem_u32(&full[r.at]), parity = r.parity;
+        if (sh.sf_slots < sh.stages) {
+          if (begun == sh.sf_slots) {
+            if (lane >= 16u) bar = smem_u32(&empty[sf_last.at]), parity = sf_last.parity;
+            sf_last.next(sh.stages);
+          } else {
+            ++begun;
+          }
         }
-        if (!(ok = mm_wait(smem_u32(&full[r.at]), r.parity, &gave_up))) break;
+        if (!(ok = mm_wait(bar, parity, &gave_up))) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        // scales written by cp.async and plain stores: seen by the copy below
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        // scales written by cp.async and plain stores: seen by the copies below
+        if (!PAIR) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         last = r;
         any = true;
-        left -= 256u;  // wraps only after the last step
-        if (!elect_one()) continue;
-        const uint32_t at = ring + r.at * stage_at;
-        const uint32_t slot = sf_base + sf.at * sf_cols;
+        const uint32_t at = uniform(ring + r.at * stage_at);
+        const uint32_t sa = uniform(sf_base + sf.at * sf_cols), sb = sa + 4u * ATOMS;
+        const uint32_t left = uniform(sh.cols - k * 256u);
         const u64 sd = scale_desc(at + w_code + x_code);
-#pragma unroll
-        for (uint32_t j = 0; j < ATOMS; ++j) {
-          scales_to_tmem(slot + 4u * j, sd + 32u * j);
-          scales_to_tmem(slot + 4u * ATOMS + 4u * RB * j, sd + 32u * (ATOMS + j));
-          if (two)
-            scales_to_tmem(slot + 4u * ATOMS + 4u * (RB * j + 1u), sd + 32u * (2u * ATOMS + j));
-        }
         const u64 da = code_desc(at), db = code_desc(at + w_code);
+        if (elect_one()) {
 #pragma unroll
-        for (uint32_t j = 0; j < 4u; ++j) {
-          const uint32_t c = MX ? j / 2u : j;  // piece with this product's scales
-          const uint32_t id = MX ? (j & 1u) * 2u : 0u;
-          if (left + 256u > 64u * j)
-            mma_fp4<MX>(d, da + 2u * j, db + 2u * j, idesc | (id << 4) | (id << 29),
-                        slot + 4u * c, slot + 4u * ATOMS + 4u * RB * c, (k | j) != 0u);
+          for (uint32_t j = 0; j < ATOMS; ++j) {
+            scales_to_tmem<CG>(sa + 4u * j, sd + 32u * j);
+            scales_to_tmem<CG>(sb + 4u * RB * j, sd + 32u * (ATOMS + j));
+            if (two) scales_to_tmem<CG>(sb + 4u * (RB * j + 1u), sd + 32u * (2u * ATOMS + j));
+          }
+#pragma unroll
+          for (uint32_t j = 0; j < 4u; ++j) {
+            const uint32_t c = MX ? j / 2u : j;  // piece with this product's scales
+            const uint32_t id = MX ? (j & 1u) * 2u : 0u;
+            if (left > 64u * j)
+              mma_fp4<MX, CG>(d, da + 2u * j, db + 2u * j, idesc | (id << 4) | (id << 29),
+                              sa + 4u * c, sb + 4u * RB * c + shift, k > k0 || j > 0u);
+          }
+          mma_commit<CG>(smem_u32(&empty[r.at]));
         }
-        mma_commit(smem_u32(&empty[r.at]));
       }
       if (!ok) break;
-      if (elect_one()) mma_commit(smem_u32(&acc_full[acc.at]));
+      if (elect_one()) mma_commit<CG>(smem_u32(&acc_full[acc.at]));
       acc.next(sh.accs);
     }
     // the products in flight must end before tensor memory is freed
     if (any) mm_wait(smem_u32(&empty[last.at]), last.parity, &gave_up);
-  } else if (warp >= 4) {
-    const uint32_t q = warp - 4u;  // this warp's 32 lanes of tensor memory
-    uint16_t* mine = turn + q * 32u * 40u;
+  } else if (warp >= 4 && warp < 4u + 4u * OUT) {
+    // OUT warps per 32 lanes of tensor memory, each every OUT-th 16 tokens
+    const uint32_t q = warp % 4u, odd = warp / 4u - 1u;
+    uint16_t* mine = reinterpret_cast<uint16_t*>(after) + (warp - 4u) * 16u * 40u;
+    // this lane's row of a transposed store: token and 8 columns of a 16 x 16 piece
+    const uint32_t st_at =
+        smem_u32(mine + ((lane / 16u) * 8u + lane % 8u) * 40u + (lane / 8u % 2u) * 8u);
+    const uint32_t tok = lane / 4u, col = (lane % 4u) * 8u;
     Ring acc;
     bool ok = true;
-    for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const MmTile m = mm_tile(t, first_tile, offs, sh);
-      OutScale scale{1.0f, 1.0f, 1.0f};
+    for (uint32_t t = t0; ok && t < tiles; t += t_step) {
+      const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
+      OutScale scale{1.0f, 1.0f, 1.0f, true};
       if (m.product) {
         if (!MX) scale = make_out_scale(ag[m.group], wg[m.group]);
         if (!(ok = mm_wait(smem_u32(&acc_full[acc.at]), acc.parity, &gave_up))) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       }
       const uint32_t d = tmem + acc.at * acc_cols + (q << 21);
-      const uint32_t j0 = m.j0 + 32u * q;
-      for (uint32_t c0 = 0; c0 < m.tokens; c0 += 32u) {
-        uint32_t v[32];
-        if (m.product) {
-          tmem_ld16(d + c0, v);
-          tmem_ld16(d + c0 + 16u, v + 16);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) v[x] = 0u;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float f = MX ? __uint_as_float(v[x]) : scale.apply(__uint_as_float(v[x]));
-          mine[x * 40 + lane] = (uint16_t)cvt_bf16x2(f, 0.0f);
-        }
-        __syncwarp();
-        const uint32_t last = min(32u, m.tokens - c0);
-        if (sh.out16) {
-#pragma unroll
-          for (uint32_t p = 0; p < 4u; ++p) {
-            const uint32_t tok = p * 8u + lane / 4u, col = (lane % 4u) * 8u;
-            if (tok < last && (int64_t)j0 + col < sh.n)
-              *reinterpret_cast<uint4*>(out + (size_t)(m.row0 + c0 + tok) * sh.n + j0 + col) =
-                  *reinterpret_cast<const uint4*>(mine + tok * 40u + col);
-          }
-        } else if ((int64_t)j0 + lane < sh.n) {
-          for (uint32_t tok = 0; tok < last; ++tok)
-            out[(size_t)(m.row0 + c0 + tok) * sh.n + j0 + lane] = mine[tok * 40u + lane];
-        }
-      }
+      const uint32_t j0 = m.j0 + j_rank + 32u * q;
+      uint16_t* to = out + (size_t)m.row0 * sh.n + j0;
+      const uint32_t c0 = (m.lead & ~15u) + 16u * odd;
+      uint32_t w[PIECES][8];  // this warp's pieces of 16 tokens x 32 columns, as bf16 pairs
       if (m.product) {
+        uint32_t v[2][16];  // this piece's sums and the next one's, already on their way
+        if (c0 < m.tokens) tmem_ld_32x16(d + c0, v[0]);
+#pragma unroll
+        for (uint32_t i = 0; i < PIECES; ++i) {
+          const uint32_t c = c0 + 16u * OUT * i;
+          if (c >= m.tokens) break;
+          tmem_wait_ld(v[i & 1u]);
+          if (i + 1u < PIECES && c + 16u * OUT < m.tokens)
+            tmem_ld_32x16(d + c + 16u * OUT, v[(i + 1u) & 1u]);
+          if (sh.split > 1u) {  // this CTA's part of the sum, [token][128] in the free ring
+            float* part = reinterpret_cast<float*>(ring_p) + 32u * q;
+#pragma unroll
+            for (uint32_t x = 0; x < 16u; ++x)
+              part[(c + x / 4u % 2u * 8u + lane % 4u * 2u + x % 2u) * 128u + x / 8u * 16u +
+                   x / 2u % 2u * 8u + lane / 4u] = __uint_as_float(v[i & 1u][x]);
+            continue;
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            float lo = __uint_as_float(v[i & 1u][2 * x]), hi = __uint_as_float(v[i & 1u][2 * x + 1]);
+            if (!MX) lo = scale.apply(lo), hi = scale.apply(hi);
+            w[i][x] = cvt_bf16x2(lo, hi);
+          }
+        }
+        // the accumulator is free before any of it is stored
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&acc_empty[acc.at]));
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_peer(peer_smem(smem_u32(&acc_empty[acc.at]), 0));
+          else
+            mbar_arrive(smem_u32(&acc_empty[acc.at]));
+        }
         acc.next(sh.accs);
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < PIECES; ++i)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[i][x] = 0u;
+      }
+      if (sh.split > 1u) continue;
+#pragma unroll
+      for (uint32_t i = 0; i < PIECES; ++i) {
+        const uint32_t c = c0 + 16u * OUT * i;
+        if (c >= m.tokens) break;
+        __syncwarp();
+        st_matrix_t(st_at, w[i][0], w[i][1], w[i][2], w[i][3]);
+        st_matrix_t(st_at + 32u, w[i][4], w[i][5], w[i][6], w[i][7]);
+        __syncwarp();
+        if (sh.out16) {
+#pragma unroll
+          for (uint32_t p = 0; p < 16u; p += 8u) {
+            const uint32_t row = c + tok + p;
+            if (row >= m.lead && row < m.tokens && (int64_t)j0 + col < sh.n)
+              *reinterpret_cast<uint4*>(to + (size_t)row * sh.n + col) =
+                  *reinterpret_cast<const uint4*>(mine + (tok + p) * 40u + col);
+          }
+        } else if ((int64_t)j0 + lane < sh.n) {
+          const uint32_t last = min(c + 16u, m.tokens);
+          for (uint32_t row = max(c, m.lead); row < last; ++row)
+            to[(size_t)row * sh.n + lane] = mine[(row - c) * 40u + lane];
+        }
+      }
+    }
+  }
+  if (sh.split > 1u) {
+    // Every CTA of the cluster holds a part of the sums of one tile; each adds
+    // up every split-th token, the parts in the order of k.
+    cluster_sync();
+    if (t0 < tiles) {
+      const MmTile m = mm_tile<CG>(t0, first_tile, offs, sh);
+      const OutScale scale =
+          MX ? OutScale{1.0f, 1.0f, 1.0f, true} : make_out_scale(ag[m.group], wg[m.group]);
+      const uint32_t j = threadIdx.x % 128u;
+      for (uint32_t tk = rank + threadIdx.x / 128u * sh.split; tk < m.tokens;
+           tk += kMmThreads / 128u * sh.split) {
+        const uint32_t word = ring + (tk * 128u + j) * 4u;
+        float v[8], sum = 0.0f;  // up to 8 parts, read at once
+#pragma unroll
+        for (uint32_t s = 0; s < 8u; ++s)
+          if (s < sh.split) v[s] = ld_peer(peer_smem(word, s));
+#pragma unroll
+        for (uint32_t s = 0; s < 8u; ++s)
+          if (s < sh.split) sum += v[s];
+        if (!MX) sum = scale.apply(sum);
+        if ((int64_t)m.j0 + j < sh.n)
+          out[(size_t)(m.row0 + tk) * sh.n + m.j0 + j] = (uint16_t)cvt_bf16x2(sum, 0.0f);
       }
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  // no CTA leaves while another reads its memory, signals it or multiplies its stages
+  if (PAIR || sh.split > 1u) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(kMmTmemCols));
+  if (warp == 1) {
+    if (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(kMmTmemCols));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(kMmTmemCols));
+  }
 }

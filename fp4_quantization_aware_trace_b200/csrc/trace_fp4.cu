@@ -330,6 +330,23 @@ int code_map(CUtensorMap* map, const uint8_t* codes, uint64_t rows, uint64_t byt
              : TRACE_ERR_CUDA;
 }
 
+// Tiled scales as rows of 8-byte words, one row per 128-row block, copied in
+// boxes of `atoms` 512-byte pieces.
+int scale_map(CUtensorMap* map, const uint8_t* scales, uint64_t rows, uint32_t scols,
+              uint32_t atoms) {
+  const EncodeTiled encode = encode_tiled();
+  if (encode == nullptr) return TRACE_ERR_CUDA;
+  const uint64_t pieces = (scols + 3u) / 4u;
+  const cuuint64_t dims[2] = {pieces * 64u, (rows + 127u) / 128u}, strides[1] = {pieces * 512u};
+  const cuuint32_t box[2] = {atoms * 64u, 1}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, (void*)scales, dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? TRACE_OK
+             : TRACE_ERR_CUDA;
+}
+
 template <bool MX>
 int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gscale,
                   int64_t rows, int64_t cols, int32_t groups, const int64_t* offs, int a_layout,
@@ -347,55 +364,78 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   sh.groups = groups;
   sh.matrices = matrices;
   const int64_t mean = (rows + groups - 1) / groups;
-  sh.nt = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : 192;
-  sh.n_tiles = (uint32_t)((n + kMmM - 1) / kMmM);
+  sh.nt = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : kMmTokens;
+  sh.a_tiled = a_layout == TRACE_SCALES_TILED_128x4;
+  sh.w_tiled = w_layout == TRACE_SCALES_TILED_128x4;
+  // Two CTAs to a tile where tiles are large and the copy engine can take every
+  // scale: tiled layouts, whole 64s of k (a piece of four scale columns that
+  // ends inside a product would bring its padding), matrices of whole blocks.
+  const bool pair = mean > 128 && n > kMmM && sh.a_tiled && sh.w_tiled && cols % 64 == 0 &&
+                    (matrices == 1 || n % kMmM == 0);
+  const uint32_t cg = pair ? 2 : 1;
+  if (pair) sh.nt = kMmPairTokens;
+  sh.n_tiles = (uint32_t)((n + cg * kMmM - 1) / (cg * kMmM));
   sh.ksteps = (uint32_t)((cols + 2 * kMmStageBytes - 1) / (2 * kMmStageBytes));
-  sh.accs = 2;
+  sh.accs = sh.nt > 128 ? 1 : 2;
   const uint32_t rb = (sh.nt + 127) / 128;
   const uint32_t stage =
-      ((kMmM + sh.nt) * kMmStageBytes + kAtoms * 512u * (1 + rb) + 1023u) & ~1023u;
-  const uint32_t fixed = 1024u + 4 * 32 * 40 * 2 + 4u * (uint32_t)(groups + 1);
+      ((kMmM + sh.nt / cg) * kMmStageBytes + kAtoms * 512u * (1 + rb) + 1023u) & ~1023u;
+  const uint32_t fixed = 1024u + kMmTurnBytes + 4u * (uint32_t)(groups + 1);
   sh.stages = (kSmem - 1024u - fixed) / stage;
   if (sh.stages > (uint32_t)kMmMaxStages) sh.stages = kMmMaxStages;
   sh.sf_slots = (kMmTmemCols - sh.accs * ((sh.nt + 31u) & ~31u)) / (4u * kAtoms * (1 + rb));
   if (sh.sf_slots > sh.stages) sh.sf_slots = sh.stages;
-  sh.a_tiled = a_layout == TRACE_SCALES_TILED_128x4;
-  sh.w_tiled = w_layout == TRACE_SCALES_TILED_128x4;
+  const long double tiles = groups == 1
+      ? (long double)((rows + sh.nt - 1) / sh.nt) * sh.n_tiles
+      : ((long double)rows / sh.nt + 2.0L * groups) * (long double)sh.n_tiles;
+  if (tiles >= 2147483648.0L) return TRACE_ERR_SHAPE;
+  sh.split = 1;
+  if (groups == 1 && !pair)
+    while (sh.split < 8 && tiles * (sh.split * 2) <= 128 && sh.ksteps >= sh.split * 2)
+      sh.split *= 2;
   sh.a_bytes = !sh.a_tiled && (sh.scols % 4 != 0 || !aligned(a_scales, 4));
   sh.w_bytes = !sh.w_tiled && (sh.scols % 4 != 0 || !aligned(w_scales, 4));
   sh.out16 = n % 8 == 0;
-  const long double tiles =
-      ((long double)rows / sh.nt + groups) * (long double)sh.n_tiles;
-  if (tiles >= 2147483648.0L) return TRACE_ERR_SHAPE;
-  CUtensorMap a_map, w_map;
-  int st = code_map(&a_map, a_codes, (uint64_t)rows, (uint64_t)cols / 2, sh.nt);
-  if (!st) st = code_map(&w_map, w_codes, (uint64_t)n * matrices, (uint64_t)cols / 2, kMmM);
+  MmMaps maps;
+  int st = code_map(&maps.a, a_codes, (uint64_t)rows, (uint64_t)cols / 2, sh.nt / cg);
+  if (!st) st = code_map(&maps.w, w_codes, (uint64_t)n * matrices, (uint64_t)cols / 2, kMmM);
+  if (!st && pair) st = scale_map(&maps.as, a_scales, (uint64_t)rows, sh.scols, kAtoms);
+  if (!st && pair) st = scale_map(&maps.ws, w_scales, (uint64_t)n * matrices, sh.scols, kAtoms);
   if (st) return st;
   static bool attr_set[kMaxDevices];  // benign race: same value
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TRACE_ERR_CUDA;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(k_matmul<MX, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(k_matmul<MX, 1, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kSmem - 1024u)) != cudaSuccess ||
-        cudaFuncSetAttribute(k_matmul<MX, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(k_matmul<MX, 2, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kSmem - 1024u)) != cudaSuccess ||
+        cudaFuncSetAttribute(k_matmul<MX, 2, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kSmem - 1024u)) != cudaSuccess)
       return TRACE_ERR_CUDA;
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  const uint32_t most = groups == 1 ? (uint32_t)tiles : (uint32_t)sms;
-  cfg.gridDim = dim3(most < (uint32_t)sms ? (most > 0 ? most : 1) : (uint32_t)sms);
+  const uint32_t team = pair ? 2 : sh.split;  // CTAs of a cluster
+  const uint32_t teams = (uint32_t)sms / team;
+  cfg.gridDim = dim3(team * (tiles < teams && groups == 1 ? (uint32_t)tiles : teams));
   cfg.blockDim = dim3(kMmThreads);
   cfg.dynamicSmemBytes = sh.stages * stage + fixed;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = team;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rb == 1 ? k_matmul<MX, 1> : k_matmul<MX, 2>, a_map, w_map, a_scales, w_scales, a_gscale,
-                            w_gscale, groups > 1 ? offs : (const int64_t*)nullptr, sh, out) ==
-                 cudaSuccess
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg,
+                            pair      ? k_matmul<MX, 2, 2>
+                            : rb == 1 ? k_matmul<MX, 1, 1>
+                                      : k_matmul<MX, 2, 1>,
+                            maps, a_scales, w_scales, a_gscale, w_gscale,
+                            groups > 1 ? offs : (const int64_t*)nullptr, sh, out) == cudaSuccess
              ? TRACE_OK
              : TRACE_ERR_CUDA;
 }
