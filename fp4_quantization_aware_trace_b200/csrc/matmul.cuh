@@ -70,6 +70,23 @@ struct OutScale {
   }
 };
 
+// 32 x 16 sums of a piece (tmem_ld_32x16) to bf16 pairs.
+template <bool MX>
+__device__ __forceinline__ void scaled_bf16(const uint32_t* v, const OutScale& s, uint32_t* w) {
+  if (MX || s.one) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      float lo = __uint_as_float(v[2 * x]), hi = __uint_as_float(v[2 * x + 1]);
+      if (!MX) lo *= s.m, hi *= s.m;
+      w[x] = cvt_bf16x2(lo, hi);
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      w[x] = cvt_bf16x2(s.apply(__uint_as_float(v[2 * x])), s.apply(__uint_as_float(v[2 * x + 1])));
+  }
+}
+
 __device__ __forceinline__ OutScale make_out_scale(float ga, float gw) {
   const double d = (double)ga * (double)gw;  // exact
   OutScale s{(float)d, 1.0f, 1.0f, true};
@@ -152,6 +169,18 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
   return ok != 0u;
 }
 
+// Whether a phase has ended, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+
 // Bounded wait of a warp for a phase (lanes may name different barriers);
 // false once any wait of the CTA has given up.  60 cycles where the phase has
 // ended, against 90 of a loop over single polls.
@@ -202,14 +231,14 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_
 
 // Shared-memory matrix descriptors: codes with 128-byte rows in the 128-byte
 // swizzle (8-row groups 1024 bytes apart); scales as 32 rows of 16 bytes
-// (8-row groups 128 bytes apart, no swizzle).
-__device__ __forceinline__ u64 code_desc(uint32_t smem) {
-  return (u64)((smem & 0x3FFFFu) >> 4) | ((u64)1 << 16) | ((u64)(1024 >> 4) << 32) |
-         ((u64)1 << 46) | ((u64)2 << 61);
+// (8-row groups 128 bytes apart, no swizzle).  The upper words are constants,
+// the lower ones hold the address in 16-byte units.
+constexpr uint32_t kCodeDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kScaleDescHigh = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t code_desc(uint32_t smem) {
+  return ((smem & 0x3FFFFu) >> 4) | (1u << 16);
 }
-__device__ __forceinline__ u64 scale_desc(uint32_t smem) {
-  return (u64)((smem & 0x3FFFFu) >> 4) | ((u64)(128 >> 4) << 32) | ((u64)1 << 46);
-}
+__device__ __forceinline__ uint32_t scale_desc(uint32_t smem) { return (smem & 0x3FFFFu) >> 4; }
 
 // Instruction descriptor: E2M1 x E2M1, K-major, M = 128 per CTA, N = n; the
 // scale type (the ids of the bytes used in a scale word are added later).
@@ -227,15 +256,17 @@ __device__ __forceinline__ uint32_t mm_width(uint32_t tokens) {
 
 // D += A B on one CTA's tensor core or (CG 2) on a pair's: each CTA then
 // holds its 128 rows of A, half the rows of B, and its rows of D.
-#define TRACE_MMA_FP4(GROUP, KIND, VEC)                                                   \
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"                        \
-               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND ".block_scale.scale_vec::" VEC \
-               " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                         \
-               "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)            \
+#define TRACE_MMA_FP4(GROUP, KIND, VEC)                                                       \
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\t"           \
+               "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"                            \
+               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND ".block_scale.scale_vec::" VEC   \
+               " [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),                               \
+               "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add),               \
+               "n"(kCodeDescHigh)                                                              \
                : "memory")
 template <bool MX, int CG>
-__device__ __forceinline__ void mma_fp4(uint32_t d, u64 a, u64 b, uint32_t idesc, uint32_t sa,
-                                        uint32_t sb, bool add) {
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        uint32_t sa, uint32_t sb, bool add) {
   if (MX && CG == 1) TRACE_MMA_FP4("1", "mxf4", "2X");
   if (MX && CG == 2) TRACE_MMA_FP4("2", "mxf4", "2X");
   if (!MX && CG == 1) TRACE_MMA_FP4("1", "mxf4nvf4", "4X");
@@ -246,12 +277,16 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, u64 a, u64 b, uint32_t idesc
 // 512 bytes of scales to 4 columns of tensor memory (CG 2: each CTA of the
 // pair its own).
 template <int CG>
-__device__ __forceinline__ void scales_to_tmem(uint32_t tmem, u64 desc) {
+__device__ __forceinline__ void scales_to_tmem(uint32_t tmem, uint32_t desc) {
   if (CG == 1)
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+    asm volatile("{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\t"
+                 "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], a;\n\t}" ::"r"(tmem),
+                 "r"(desc), "n"(kScaleDescHigh)
                  : "memory");
   else
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+    asm volatile("{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\t"
+                 "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], a;\n\t}" ::"r"(tmem),
+                 "r"(desc), "n"(kScaleDescHigh)
                  : "memory");
 }
 
@@ -642,8 +677,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     Ring r, acc, sf, sf_last;  // sf_last: the stage that used the scale slot before
     acc.parity = 1u;
     uint32_t begun = 0;  // scale slots used so far, up to sf_slots
-    bool ok = true, any = false;
-    Ring last;
+    const bool sf_wait = sh.sf_slots < sh.stages;
+    // What a stage has to wait for: that it is full, and that the scale slot's
+    // last reader is done; half of the lanes wait for each (with a slot for
+    // every stage the first says the second).  The next stage's barriers are
+    // tested before this stage's instructions are issued, so that the answer
+    // has arrived when they have been.
+    uint32_t bar = smem_u32(&full[0]), parity = 0u;
+    bool ok = true, ready = false, any = false;
+    uint32_t at = ring, freed = 0u, freed_parity = 0u;
     for (uint32_t t = t0; ok && t < tiles; t += t_step) {
       const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       if (!m.product) continue;
@@ -651,56 +693,64 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       const uint32_t d = uniform(tmem + acc.at * acc_cols), idesc = mm_idesc<MX, CG>(width);
       // tokens that start in the middle of a block: two columns of scales on
       const uint32_t shift = PAIR ? uniform((uint32_t)(m.row0 % 128) / 32u) : 0u;
-      const bool two = RB == 2 && 32u * shift + width > 128u;
       if (!(ok = mm_wait(smem_u32(&acc_empty[acc.at]), acc.parity, &gave_up))) break;
-      for (uint32_t k = k0; k < k1; ++k, r.next(sh.stages), sf.next(sh.sf_slots)) {
-        // The stage is full, and the scale slot's last reader is done: half of
-        // the lanes wait for each (with a slot for every stage the first says
-        // the second).
-        uint32_t bar = smem_u32(&full[r.at]), parity = r.parity;
-        if (sh.sf_slots < sh.stages) {
-          if (begun == sh.sf_slots) {
-            if (lane >= 16u) bar = smem_u32(&empty[sf_last.at]), parity = sf_last.parity;
-            sf_last.next(sh.stages);
-          } else {
-            ++begun;
-          }
-        }
-        if (!(ok = mm_wait(bar, parity, &gave_up))) break;
+      for (uint32_t k = k0; k < k1; ++k) {
+        if (!__all_sync(0xFFFFFFFFu, ready)) ok = ok && mm_wait(bar, parity, &gave_up);
+        if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         // scales written by cp.async and plain stores: seen by the copies below
         if (!PAIR) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        last = r;
+        const uint32_t now = uniform(at), sa = uniform(sf_base + sf.at * sf_cols);
+        const uint32_t sb = sa + 4u * ATOMS, sd = scale_desc(now + w_code + x_code);
+        const uint32_t da = code_desc(now), db = code_desc(now + w_code);
+        const uint32_t left = sh.cols - k * 256u, more = k - k0;
+        freed = smem_u32(&empty[r.at]), freed_parity = r.parity;
         any = true;
-        const uint32_t at = uniform(ring + r.at * stage_at);
-        const uint32_t sa = uniform(sf_base + sf.at * sf_cols), sb = sa + 4u * ATOMS;
-        const uint32_t left = uniform(sh.cols - k * 256u);
-        const u64 sd = scale_desc(at + w_code + x_code);
-        const u64 da = code_desc(at), db = code_desc(at + w_code);
+        r.next(sh.stages);
+        sf.next(sh.sf_slots);
+        at = r.at == 0u ? ring : at + stage_at;
+        bar = smem_u32(&full[r.at]), parity = r.parity;
+        if (sf_wait && ++begun >= sh.sf_slots) {
+          if (lane >= 16u) bar = smem_u32(&empty[sf_last.at]), parity = sf_last.parity;
+          sf_last.next(sh.stages);
+        }
+        ready = mbar_test(bar, parity);
         if (elect_one()) {
+          // A second block that the tile does not reach is copied all the same:
+          // into columns that no product reads.
 #pragma unroll
           for (uint32_t j = 0; j < ATOMS; ++j) {
             scales_to_tmem<CG>(sa + 4u * j, sd + 32u * j);
             scales_to_tmem<CG>(sb + 4u * RB * j, sd + 32u * (ATOMS + j));
-            if (two) scales_to_tmem<CG>(sb + 4u * (RB * j + 1u), sd + 32u * (2u * ATOMS + j));
+            if (RB == 2) scales_to_tmem<CG>(sb + 4u * (RB * j + 1u), sd + 32u * (2u * ATOMS + j));
           }
+          if (left >= 256u) {
 #pragma unroll
-          for (uint32_t j = 0; j < 4u; ++j) {
-            const uint32_t c = MX ? j / 2u : j;  // piece with this product's scales
-            const uint32_t id = MX ? (j & 1u) * 2u : 0u;
-            if (left > 64u * j)
+            for (uint32_t j = 0; j < 4u; ++j) {
+              const uint32_t c = MX ? j / 2u : j;  // piece with this product's scales
+              const uint32_t id = MX ? (j & 1u) * 2u : 0u;
               mma_fp4<MX, CG>(d, da + 2u * j, db + 2u * j, idesc | (id << 4) | (id << 29),
-                              sa + 4u * c, sb + 4u * RB * c + shift, k > k0 || j > 0u);
+                              sa + 4u * c, sb + 4u * RB * c + shift, j > 0u || more > 0u);
+            }
+          } else {  // the end of k, 64 elements at a time
+#pragma unroll 1
+            for (uint32_t j = 0; 64u * j < left; ++j) {
+              const uint32_t c = MX ? j / 2u : j;
+              const uint32_t id = MX ? (j & 1u) * 2u : 0u;
+              mma_fp4<MX, CG>(d, da + 2u * j, db + 2u * j, idesc | (id << 4) | (id << 29),
+                              sa + 4u * c, sb + 4u * RB * c + shift, j > 0u || more > 0u);
+            }
           }
-          mma_commit<CG>(smem_u32(&empty[r.at]));
+          mma_commit<CG>(freed);
         }
+        __syncwarp();
       }
       if (!ok) break;
       if (elect_one()) mma_commit<CG>(smem_u32(&acc_full[acc.at]));
       acc.next(sh.accs);
     }
     // the products in flight must end before tensor memory is freed
-    if (any) mm_wait(smem_u32(&empty[last.at]), last.parity, &gave_up);
+    if (any) mm_wait(freed, freed_parity, &gave_up);
   } else if (warp >= 4 && warp < 4u + 4u * OUT) {
     // OUT warps per 32 lanes of tensor memory, each every OUT-th 16 tokens
     const uint32_t q = warp % 4u, odd = warp / 4u - 1u;
@@ -742,12 +792,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                    x / 2u % 2u * 8u + lane / 4u] = __uint_as_float(v[i & 1u][x]);
             continue;
           }
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            float lo = __uint_as_float(v[i & 1u][2 * x]), hi = __uint_as_float(v[i & 1u][2 * x + 1]);
-            if (!MX) lo = scale.apply(lo), hi = scale.apply(hi);
-            w[i][x] = cvt_bf16x2(lo, hi);
-          }
+          scaled_bf16<MX>(v[i & 1u], scale, w[i]);
         }
         // the accumulator is free before any of it is stored
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
