@@ -327,10 +327,13 @@ __device__ __forceinline__ void st_matrix_t(uint32_t addr, uint32_t a, uint32_t 
                : "memory");
 }
 
-// Every load so far has arrived; the words pass through, so that no use of
-// them moves in front of the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
+// Every load so far has arrived; no use of the words moves in front of the
+// wait, through which they pass.
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t* v) {
+  asm volatile(""
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
                  "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
                  "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
@@ -376,25 +379,46 @@ __device__ __forceinline__ int64_t mm_start(int64_t bound) {
   return CG == 2 ? bound & ~(int64_t)127 : bound;
 }
 
+// A role's walk over its tiles: token tile and w tile, t0 and every t_step-th
+// tile after it, without a division per tile.
+struct MmWalk {
+  uint32_t tt, jt, dt, dj, n_tiles;
+  __device__ __forceinline__ MmWalk(uint32_t t0, uint32_t t_step, uint32_t n)
+      : tt(t0 / n), jt(t0 % n), dt(t_step / n), dj(t_step % n), n_tiles(n) {}
+  __device__ __forceinline__ void next() {
+    tt += dt;
+    jt += dj;
+    if (jt >= n_tiles) {
+      jt -= n_tiles;
+      ++tt;
+    }
+  }
+};
+
+// For a converged warp: with several groups its lanes search the table
+// together, 32 entries at a time.
 template <int CG>
-__device__ __forceinline__ MmTile mm_tile(uint32_t t, const uint32_t* first_tile,
+__device__ __forceinline__ MmTile mm_tile(const MmWalk& at, const uint32_t* first_tile,
                                           const int64_t* offs, const MmShape& sh) {
   MmTile m;
-  const uint32_t tt = t / sh.n_tiles;
-  int32_t lo = 0, hi = sh.groups - 1;  // the last group that starts at or before tt
-  while (lo < hi) {
-    const int32_t mid = (lo + hi + 1) / 2;
-    if (first_tile[mid] <= tt) lo = mid; else hi = mid - 1;
+  const uint32_t tt = at.tt;
+  uint32_t lo = 0;  // the last group that starts at or before tt
+  for (uint32_t span = (uint32_t)sh.groups; span > 1u;) {
+    const uint32_t step = (span + 31u) / 32u, probe = threadIdx.x % 32u * step;
+    const bool in = probe < span && first_tile[lo + probe] <= tt;
+    const uint32_t skip = (__popc(__ballot_sync(0xFFFFFFFFu, in)) - 1u) * step;
+    lo += skip;
+    span = min(step, span - skip);
   }
-  m.group = lo;
-  const int64_t begin = mm_bound(offs, lo, sh);
+  m.group = (int32_t)lo;
+  const int64_t begin = mm_bound(offs, m.group, sh);
   const int64_t from = mm_start<CG>(begin) + (int64_t)(tt - first_tile[lo]) * sh.nt;
   m.row0 = CG == 2 && begin - from >= 64 ? from + 64 : from;
   m.lead = begin > m.row0 ? (uint32_t)(begin - m.row0) : 0u;
-  const int64_t end = mm_bound(offs, lo + 1, sh);
+  const int64_t end = mm_bound(offs, m.group + 1, sh);
   m.tokens = (uint32_t)((end < from + sh.nt ? end : from + sh.nt) - m.row0);
-  m.j0 = (t - tt * sh.n_tiles) * (CG * kMmM);
-  m.product = lo < sh.matrices;
+  m.j0 = at.jt * (CG * kMmM);
+  m.product = m.group < sh.matrices;
   return m;
 }
 
@@ -515,7 +539,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   constexpr uint32_t block_bytes = ATOMS * 512u;  // a block's scales per stage
   constexpr bool PAIR = CG == 2;
   constexpr uint32_t OUT = PAIR ? 3u : 2u;  // warps that write out, per quarter of a tile's rows
-  constexpr uint32_t PIECES = ((PAIR ? kMmPairTokens : kMmTokens) / 16u + OUT - 1u) / OUT;
+  constexpr uint32_t PIECES = ((PAIR ? kMmPairTokens : RB == 2 ? kMmTokens : 128u) / 16u + OUT - 1u) / OUT;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) u64 full[kMmMaxStages], empty[kMmMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base_s, warp_sum[kMmThreads / 32];
@@ -564,7 +588,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   if (PAIR) cluster_sync();  // the other CTA's barriers exist
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = uniform(tmem_base_s);
-  const uint32_t tiles = first_tile[sh.groups] * sh.n_tiles;
+  const uint32_t token_tiles = first_tile[sh.groups];
   const uint32_t acc_cols = (sh.nt + 31u) & ~31u;
   constexpr uint32_t sf_cols = 4u * ATOMS * (1u + RB);  // tensor-memory columns of a stage's scales
   const uint32_t sf_base = tmem + sh.accs * acc_cols;
@@ -580,7 +604,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     r.parity = 1u;  // the first round finds every slot empty
     bool ok = true;
     const uint32_t c4s = (sh.scols + 3u) / 4u, bulk_steps = sh.scols / (4u * ATOMS);
-    for (uint32_t t = t0; ok && t < tiles; t += t_step) {
+    for (MmWalk t(t0, t_step, sh.n_tiles); ok && t.tt < token_tiles; t.next()) {
       const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       if (!m.product) continue;
       const int64_t wr = m.group * sh.n + m.j0 + j_rank;
@@ -642,7 +666,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     Ring r;
     r.parity = 1u;
     bool ok = true;
-    for (uint32_t t = t0; ok && t < tiles; t += t_step) {
+    for (MmWalk t(t0, t_step, sh.n_tiles); ok && t.tt < token_tiles; t.next()) {
       const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       if (!m.product) continue;
       const int64_t wr = m.group * sh.n + m.j0 + j_rank;
@@ -686,7 +710,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     uint32_t bar = smem_u32(&full[0]), parity = 0u;
     bool ok = true, ready = false, any = false;
     uint32_t at = ring, freed = 0u, freed_parity = 0u;
-    for (uint32_t t = t0; ok && t < tiles; t += t_step) {
+    for (MmWalk t(t0, t_step, sh.n_tiles); ok && t.tt < token_tiles; t.next()) {
       const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       if (!m.product) continue;
       const uint32_t width = uniform(mm_width<CG>(m.tokens));
@@ -761,7 +785,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const uint32_t tok = lane / 4u, col = (lane % 4u) * 8u;
     Ring acc;
     bool ok = true;
-    for (uint32_t t = t0; ok && t < tiles; t += t_step) {
+    for (MmWalk t(t0, t_step, sh.n_tiles); ok && t.tt < token_tiles; t.next()) {
       const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       OutScale scale{1.0f, 1.0f, 1.0f, true};
       if (m.product) {
@@ -773,28 +797,16 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       const uint32_t j0 = m.j0 + j_rank + 32u * q;
       uint16_t* to = out + (size_t)m.row0 * sh.n + j0;
       const uint32_t c0 = (m.lead & ~15u) + 16u * odd;
-      uint32_t w[PIECES][8];  // this warp's pieces of 16 tokens x 32 columns, as bf16 pairs
+      // This warp's pieces of 32 columns x 16 tokens: all of them leave tensor
+      // memory at once, and the accumulator is free before any is stored.
+      uint32_t v[PIECES][16];
       if (m.product) {
-        uint32_t v[2][16];  // this piece's sums and the next one's, already on their way
-        if (c0 < m.tokens) tmem_ld_32x16(d + c0, v[0]);
 #pragma unroll
-        for (uint32_t i = 0; i < PIECES; ++i) {
-          const uint32_t c = c0 + 16u * OUT * i;
-          if (c >= m.tokens) break;
-          tmem_wait_ld(v[i & 1u]);
-          if (i + 1u < PIECES && c + 16u * OUT < m.tokens)
-            tmem_ld_32x16(d + c + 16u * OUT, v[(i + 1u) & 1u]);
-          if (sh.split > 1u) {  // this CTA's part of the sum, [token][128] in the free ring
-            float* part = reinterpret_cast<float*>(ring_p) + 32u * q;
+        for (uint32_t i = 0; i < PIECES; ++i)
+          tmem_ld_32x16(d + c0 + 16u * OUT * i, v[i]);
+        tmem_wait_ld();
 #pragma unroll
-            for (uint32_t x = 0; x < 16u; ++x)
-              part[(c + x / 4u % 2u * 8u + lane % 4u * 2u + x % 2u) * 128u + x / 8u * 16u +
-                   x / 2u % 2u * 8u + lane / 4u] = __uint_as_float(v[i & 1u][x]);
-            continue;
-          }
-          scaled_bf16<MX>(v[i & 1u], scale, w[i]);
-        }
-        // the accumulator is free before any of it is stored
+        for (uint32_t i = 0; i < PIECES; ++i) tmem_arrived(v[i]);
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
@@ -808,16 +820,25 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 #pragma unroll
         for (uint32_t i = 0; i < PIECES; ++i)
 #pragma unroll
-          for (int x = 0; x < 8; ++x) w[i][x] = 0u;
+          for (int x = 0; x < 16; ++x) v[i][x] = 0u;
       }
-      if (sh.split > 1u) continue;
 #pragma unroll
       for (uint32_t i = 0; i < PIECES; ++i) {
         const uint32_t c = c0 + 16u * OUT * i;
         if (c >= m.tokens) break;
+        if (sh.split > 1u) {  // this CTA's part of the sum, [token][128] in the free ring
+          float* part = reinterpret_cast<float*>(ring_p) + 32u * q;
+#pragma unroll
+          for (uint32_t x = 0; x < 16u; ++x)
+            part[(c + x / 4u % 2u * 8u + lane % 4u * 2u + x % 2u) * 128u + x / 8u * 16u +
+                 x / 2u % 2u * 8u + lane / 4u] = __uint_as_float(v[i][x]);
+          continue;
+        }
+        uint32_t w[8];
+        scaled_bf16<MX>(v[i], scale, w);
         __syncwarp();
-        st_matrix_t(st_at, w[i][0], w[i][1], w[i][2], w[i][3]);
-        st_matrix_t(st_at + 32u, w[i][4], w[i][5], w[i][6], w[i][7]);
+        st_matrix_t(st_at, w[0], w[1], w[2], w[3]);
+        st_matrix_t(st_at + 32u, w[4], w[5], w[6], w[7]);
         __syncwarp();
         if (sh.out16) {
 #pragma unroll
@@ -839,8 +860,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     // Every CTA of the cluster holds a part of the sums of one tile; each adds
     // up every split-th token, the parts in the order of k.
     cluster_sync();
-    if (t0 < tiles) {
-      const MmTile m = mm_tile<CG>(t0, first_tile, offs, sh);
+    const MmWalk t(t0, t_step, sh.n_tiles);
+    if (t.tt < token_tiles) {
+      const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       const OutScale scale =
           MX ? OutScale{1.0f, 1.0f, 1.0f, true} : make_out_scale(ag[m.group], wg[m.group]);
       const uint32_t j = threadIdx.x % 128u;
