@@ -34,6 +34,9 @@ constexpr int kMmM = 128;            // w rows of a tile
 constexpr int kMmStageBytes = 128;   // code bytes per row and stage: 256 elements
 constexpr int kMmMaxStages = 8;
 constexpr uint32_t kMmTurnBytes = 12 * 16 * 40 * 2;  // output pieces being transposed
+// CTAs that share a tile's k: clusters of 8 take 5 us longer to launch than
+// clusters of 4 (29 x 2048 x 4096: 12.9 us with 8, 7.6 with 4, 10.7 with 1).
+constexpr uint32_t kMmMaxSplit = 4;
 constexpr uint32_t kMmTokens = 192, kMmPairTokens = 256;  // of the largest tiles
 constexpr uint32_t kMmTmemCols = 512;
 // Polls of one wait before a CTA gives up (each try_wait itself suspends):
@@ -48,6 +51,7 @@ struct MmShape {
   uint32_t n_tiles;            // ceil(n / 128), of pairs ceil(n / 256)
   uint32_t ksteps;             // stages of a whole product
   uint32_t stages, accs, sf_slots;
+  uint32_t step_tokens, step_j;  // token and w tiles from one of a CTA's (a team's) to its next
   uint32_t split;              // CTAs of a cluster that share one tile's k (1: none)
   uint8_t a_tiled, w_tiled;
   uint8_t a_bytes, w_bytes;    // row-major scales that are not 4-byte words
@@ -192,6 +196,10 @@ __device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, volatile 
   *gave_up = 1u;
   g_matmul_gave_up = 1u;
   return false;
+}
+
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // CG 2: `bar` may lie in the other CTA of the pair.
@@ -383,8 +391,10 @@ __device__ __forceinline__ int64_t mm_start(int64_t bound) {
 // tile after it, without a division per tile.
 struct MmWalk {
   uint32_t tt, jt, dt, dj, n_tiles;
-  __device__ __forceinline__ MmWalk(uint32_t t0, uint32_t t_step, uint32_t n)
-      : tt(t0 / n), jt(t0 % n), dt(t_step / n), dj(t_step % n), n_tiles(n) {}
+  __device__ __forceinline__ MmWalk(uint32_t t0, const MmShape& sh)
+      : tt(t0 / sh.n_tiles), dt(sh.step_tokens), dj(sh.step_j), n_tiles(sh.n_tiles) {
+    jt = t0 - tt * n_tiles;
+  }
   __device__ __forceinline__ void next() {
     tt += dt;
     jt += dj;
@@ -412,7 +422,8 @@ __device__ __forceinline__ MmTile mm_tile(const MmWalk& at, const uint32_t* firs
   }
   m.group = (int32_t)lo;
   const int64_t begin = mm_bound(offs, m.group, sh);
-  const int64_t from = mm_start<CG>(begin) + (int64_t)(tt - first_tile[lo]) * sh.nt;
+  const uint32_t first = sh.groups > 1 ? first_tile[lo] : 0u;
+  const int64_t from = mm_start<CG>(begin) + (int64_t)(tt - first) * sh.nt;
   m.row0 = CG == 2 && begin - from >= 64 ? from + 64 : from;
   m.lead = begin > m.row0 ? (uint32_t)(begin - m.row0) : 0u;
   const int64_t end = mm_bound(offs, m.group + 1, sh);
@@ -566,7 +577,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     gave_up = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  pdl_begin();
+  if (warp == 0 && elect_one()) {
+    tma_prefetch_map(&maps.w);
+    tma_prefetch_map(&maps.a);
+    if (PAIR) tma_prefetch_map(&maps.ws), tma_prefetch_map(&maps.as);
+  }
   if (warp == 1) {
     if (PAIR) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -582,19 +597,23 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
   }
-  mm_table<CG>(first_tile, warp_sum, offs, sh);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (PAIR) cluster_sync();  // the other CTA's barriers exist
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  pdl_begin();  // nothing before this read or wrote what another kernel may
+  uint32_t token_tiles = (uint32_t)((sh.rows + sh.nt - 1) / sh.nt);
+  if (sh.groups > 1) {
+    mm_table<CG>(first_tile, warp_sum, offs, sh);
+    token_tiles = first_tile[sh.groups];
+  }
   const uint32_t tmem = uniform(tmem_base_s);
-  const uint32_t token_tiles = first_tile[sh.groups];
   const uint32_t acc_cols = (sh.nt + 31u) & ~31u;
   constexpr uint32_t sf_cols = 4u * ATOMS * (1u + RB);  // tensor-memory columns of a stage's scales
   const uint32_t sf_base = tmem + sh.accs * acc_cols;
   // this CTA's tiles, and its part of k
   const uint32_t team = PAIR ? 2u : sh.split;
-  const uint32_t t0 = blockIdx.x / team, t_step = gridDim.x / team;
+  const uint32_t t0 = blockIdx.x / team;
   const uint32_t k_rank = PAIR ? 0u : rank;
   const uint32_t k0 = k_rank * sh.ksteps / sh.split, k1 = (k_rank + 1u) * sh.ksteps / sh.split;
   const uint32_t j_rank = PAIR ? rank * kMmM : 0u;
@@ -604,7 +623,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     r.parity = 1u;  // the first round finds every slot empty
     bool ok = true;
     const uint32_t c4s = (sh.scols + 3u) / 4u, bulk_steps = sh.scols / (4u * ATOMS);
-    for (MmWalk t(t0, t_step, sh.n_tiles); ok && t.tt < token_tiles; t.next()) {
+    for (MmWalk t(t0, sh); ok && t.tt < token_tiles; t.next()) {
       const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       if (!m.product) continue;
       const int64_t wr = m.group * sh.n + m.j0 + j_rank;
@@ -666,7 +685,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     Ring r;
     r.parity = 1u;
     bool ok = true;
-    for (MmWalk t(t0, t_step, sh.n_tiles); ok && t.tt < token_tiles; t.next()) {
+    for (MmWalk t(t0, sh); ok && t.tt < token_tiles; t.next()) {
       const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       if (!m.product) continue;
       const int64_t wr = m.group * sh.n + m.j0 + j_rank;
@@ -710,7 +729,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     uint32_t bar = smem_u32(&full[0]), parity = 0u;
     bool ok = true, ready = false, any = false;
     uint32_t at = ring, freed = 0u, freed_parity = 0u;
-    for (MmWalk t(t0, t_step, sh.n_tiles); ok && t.tt < token_tiles; t.next()) {
+    for (MmWalk t(t0, sh); ok && t.tt < token_tiles; t.next()) {
       const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       if (!m.product) continue;
       const uint32_t width = uniform(mm_width<CG>(m.tokens));
@@ -785,7 +804,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const uint32_t tok = lane / 4u, col = (lane % 4u) * 8u;
     Ring acc;
     bool ok = true;
-    for (MmWalk t(t0, t_step, sh.n_tiles); ok && t.tt < token_tiles; t.next()) {
+    for (MmWalk t(t0, sh); ok && t.tt < token_tiles; t.next()) {
       const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       OutScale scale{1.0f, 1.0f, 1.0f, true};
       if (m.product) {
@@ -860,7 +879,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     // Every CTA of the cluster holds a part of the sums of one tile; each adds
     // up every split-th token, the parts in the order of k.
     cluster_sync();
-    const MmWalk t(t0, t_step, sh.n_tiles);
+    const MmWalk t(t0, sh);
     if (t.tt < token_tiles) {
       const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
       const OutScale scale =
@@ -869,12 +888,12 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       for (uint32_t tk = rank + threadIdx.x / 128u * sh.split; tk < m.tokens;
            tk += kMmThreads / 128u * sh.split) {
         const uint32_t word = ring + (tk * 128u + j) * 4u;
-        float v[8], sum = 0.0f;  // up to 8 parts, read at once
+        float v[kMmMaxSplit], sum = 0.0f;  // the parts, read at once
 #pragma unroll
-        for (uint32_t s = 0; s < 8u; ++s)
+        for (uint32_t s = 0; s < kMmMaxSplit; ++s)
           if (s < sh.split) v[s] = ld_peer(peer_smem(word, s));
 #pragma unroll
-        for (uint32_t s = 0; s < 8u; ++s)
+        for (uint32_t s = 0; s < kMmMaxSplit; ++s)
           if (s < sh.split) sum += v[s];
         if (!MX) sum = scale.apply(sum);
         if ((int64_t)m.j0 + j < sh.n)

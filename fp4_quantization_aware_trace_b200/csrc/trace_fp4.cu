@@ -391,7 +391,7 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   if (tiles >= 2147483648.0L) return TRACE_ERR_SHAPE;
   sh.split = 1;
   if (groups == 1 && !pair)
-    while (sh.split < 8 && tiles * (sh.split * 2) <= 128 && sh.ksteps >= sh.split * 2)
+    while (sh.split < kMmMaxSplit && tiles * (sh.split * 2) <= 128 && sh.ksteps >= sh.split * 2)
       sh.split *= 2;
   sh.a_bytes = !sh.a_tiled && (sh.scols % 4 != 0 || !aligned(a_scales, 4));
   sh.w_bytes = !sh.w_tiled && (sh.scols % 4 != 0 || !aligned(w_scales, 4));
@@ -417,8 +417,11 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   }
   cudaLaunchConfig_t cfg = {};
   const uint32_t team = pair ? 2 : sh.split;  // CTAs of a cluster
-  const uint32_t teams = (uint32_t)sms / team;
-  cfg.gridDim = dim3(team * (tiles < teams && groups == 1 ? (uint32_t)tiles : teams));
+  uint32_t teams = (uint32_t)sms / team;
+  if (groups == 1 && tiles < teams) teams = (uint32_t)tiles;
+  sh.step_tokens = teams / sh.n_tiles;
+  sh.step_j = teams % sh.n_tiles;
+  cfg.gridDim = dim3(team * teams);
   cfg.blockDim = dim3(kMmThreads);
   cfg.dynamicSmemBytes = sh.stages * stage + fixed;
   cfg.stream = stream;
