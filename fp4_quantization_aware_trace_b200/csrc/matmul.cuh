@@ -743,9 +743,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         // scales written by cp.async and plain stores: seen by the copies below
         if (!PAIR) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        const uint32_t now = uniform(at), sa = uniform(sf_base + sf.at * sf_cols);
-        const uint32_t sb = sa + 4u * ATOMS, sd = scale_desc(now + w_code + x_code);
-        const uint32_t da = code_desc(now), db = code_desc(now + w_code);
+        const uint32_t sa = sf_base + sf.at * sf_cols, sb = sa + 4u * ATOMS;
+        const uint32_t sd = scale_desc(at + w_code + x_code);
+        const uint32_t da = code_desc(at), db = code_desc(at + w_code);
         const uint32_t left = sh.cols - k * 256u, more = k - k0;
         freed = smem_u32(&empty[r.at]), freed_parity = r.parity;
         any = true;
@@ -786,7 +786,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           }
           mma_commit<CG>(freed);
         }
-        __syncwarp();
       }
       if (!ok) break;
       if (elect_one()) mma_commit<CG>(smem_u32(&acc_full[acc.at]));
