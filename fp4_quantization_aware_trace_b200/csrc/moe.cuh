@@ -10,8 +10,9 @@
 #pragma once
 
 constexpr int kSortMaxWarps = 32;
-constexpr uint32_t kSortSmem = 48u * 1024u;  // per-warp counters: no opt-in needed
+constexpr uint32_t kSortSmem = 96u * 1024u;  // per-warp counters
 constexpr uint32_t kSortChunk = 4096u;       // slots per CTA; one CTA sorts as many alone
+constexpr uint32_t kSortMaxChunks = 256u;    // beyond that chunks grow: every CTA reads all counts
 
 // The counter a slot belongs to: its expert, or E for a dropped one.
 template <typename ID>
@@ -21,21 +22,50 @@ __device__ __forceinline__ uint32_t sort_key(const ID* __restrict__ ids, uint32_
   return v >= (ID)0 && (long long)v < (long long)E ? (uint32_t)v : E;
 }
 
-// First pass of a sort over several CTAs: counts of one chunk of slots.
+// First pass of a sort over several CTAs: counts of one chunk of slots,
+// counts[e][chunk].
 template <typename ID>
-__global__ void k_moe_count(const ID* __restrict__ ids, uint32_t slots, uint32_t E,
-                            uint32_t* __restrict__ counts) {
+__global__ void __launch_bounds__(512)
+    k_moe_count(const ID* __restrict__ ids, uint32_t slots, uint32_t chunk, uint32_t E,
+                uint32_t* __restrict__ counts) {
   extern __shared__ uint32_t hist[];
   pdl_begin();
   for (uint32_t e = threadIdx.x; e <= E; e += blockDim.x) hist[e] = 0u;
   __syncthreads();
-  const uint32_t first = blockIdx.x * kSortChunk;
-  const uint32_t last = min(first + kSortChunk, slots);
-  for (uint32_t s = first + threadIdx.x; s < last; s += blockDim.x)
-    atomicAdd(&hist[sort_key(ids, s, E)], 1u);
+  const uint32_t first = blockIdx.x * chunk, last = min(first + chunk, slots);
+  for (uint32_t s0 = first + threadIdx.x; s0 < last; s0 += 8u * blockDim.x) {
+    uint32_t key[8];  // eight loads on their way at a time
+#pragma unroll
+    for (uint32_t i = 0; i < 8u; ++i)
+      if (s0 + i * blockDim.x < last) key[i] = sort_key(ids, s0 + i * blockDim.x, E);
+#pragma unroll
+    for (uint32_t i = 0; i < 8u; ++i)
+      if (s0 + i * blockDim.x < last) atomicAdd(&hist[key[i]], 1u);
+  }
   __syncthreads();
   for (uint32_t e = threadIdx.x; e <= E; e += blockDim.x)
-    counts[(size_t)blockIdx.x * (E + 1u) + e] = hist[e];
+    counts[(size_t)e * gridDim.x + blockIdx.x] = hist[e];
+}
+
+// Keys of 128 slots from s0 on, 32 apart (n past the end: no counter).
+template <typename ID>
+__device__ __forceinline__ void sort_keys(const ID* __restrict__ ids, uint32_t s0, uint32_t hi,
+                                          uint32_t E, uint32_t n, uint32_t* key) {
+  const uint32_t s = s0 + threadIdx.x % 32u;
+#pragma unroll
+  for (uint32_t i = 0; i < 4u; ++i) key[i] = s + 32u * i < hi ? sort_key(ids, s + 32u * i, E) : n;
+}
+
+// Lanes of the warp with this lane's key (< 2^bits), a ballot per bit: the
+// match instruction would take 20 us of a sort of 65536 x 8 slots.
+__device__ __forceinline__ uint32_t same_key(uint32_t key, uint32_t bits) {
+  uint32_t same = 0xFFFFFFFFu;
+  for (uint32_t b = 0; b < bits; ++b) {
+    const bool one = key >> b & 1u;
+    const uint32_t ones = __ballot_sync(0xFFFFFFFFu, one);
+    same &= one ? ones : ~ones;
+  }
+  return same;
 }
 
 // Second pass (the only one when a single CTA holds every slot).  Each warp
@@ -43,30 +73,53 @@ __global__ void k_moe_count(const ID* __restrict__ ids, uint32_t slots, uint32_t
 // then become each warp's next row per expert: rows of earlier experts +
 // this expert's rows in earlier chunks + in earlier warps.  In the last
 // walk the lanes of one expert rank themselves by lane, which is slot order.
+// Bound by latencies, so a warp reads an expert's counts of all chunks at once
+// (65536 x 8 slots, 128 experts: 18 us for both passes; with a thread per
+// expert that walked its counts, and the match instruction, 26 us).
 template <typename ID>
 __global__ void __launch_bounds__(32 * kSortMaxWarps)
-    k_moe_place(const ID* __restrict__ ids, uint32_t slots, uint32_t E,
+    k_moe_place(const ID* __restrict__ ids, uint32_t slots, uint32_t chunk, uint32_t E,
                 const uint32_t* __restrict__ counts, int64_t* __restrict__ offsets,
                 int32_t* __restrict__ rows, int32_t* __restrict__ slot_of) {
-  extern __shared__ uint32_t next[];  // [warps][E + 1]
+  extern __shared__ uint32_t next[];  // [warps][E + 1], all[E + 1], earlier[E + 1]
   __shared__ uint32_t part[kSortMaxWarps];
   __shared__ uint32_t carry;
   const uint32_t n = E + 1u, warps = blockDim.x / 32u;
   const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
+  uint32_t* all = next + warps * n;
+  uint32_t* earlier = all + n;
   pdl_begin();
   for (uint32_t i = threadIdx.x; i < warps * n; i += blockDim.x) next[i] = 0u;
   if (threadIdx.x == 0) carry = 0u;
+  if (counts != nullptr)
+    for (uint32_t e = warp; e < n; e += warps) {
+      uint32_t total = 0u, before = 0u;
+      uint32_t v[kSortMaxChunks / 32u];  // all on their way at once
+#pragma unroll
+      for (uint32_t i = 0; i < kSortMaxChunks / 32u; ++i) {
+        const uint32_t c = lane + 32u * i;
+        v[i] = c < gridDim.x ? counts[(size_t)e * gridDim.x + c] : 0u;
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < kSortMaxChunks / 32u; ++i) {
+        total += v[i];
+        before += lane + 32u * i < blockIdx.x ? v[i] : 0u;
+      }
+      total = __reduce_add_sync(0xFFFFFFFFu, total);
+      before = __reduce_add_sync(0xFFFFFFFFu, before);
+      if (lane == 0) all[e] = total, earlier[e] = before;
+    }
   __syncthreads();
-  const uint32_t first = blockIdx.x * kSortChunk, last = min(first + kSortChunk, slots);
+  const uint32_t first = blockIdx.x * chunk, last = min(first + chunk, slots);
   const uint32_t piece = (last - first + warps * 32u - 1u) / (warps * 32u) * 32u;
   const uint32_t lo = min(first + warp * piece, last), hi = min(lo + piece, last);
   uint32_t* mine = next + warp * n;
-  for (uint32_t s0 = lo; s0 < hi; s0 += 32u) {
-    const bool in = s0 + lane < hi;
-    const uint32_t e = in ? sort_key(ids, s0 + lane, E) : n;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    if (in && lane == (uint32_t)__ffs((int)same) - 1u) mine[e] += __popc(same);
-    __syncwarp();
+  uint32_t key[4];
+  for (uint32_t s0 = lo; s0 < hi; s0 += 128u) {
+    sort_keys(ids, s0, hi, E, n, key);
+#pragma unroll
+    for (uint32_t i = 0; i < 4u; ++i)
+      if (key[i] < n) atomicAdd(&mine[key[i]], 1u);
   }
   __syncthreads();
   for (uint32_t e0 = 0; e0 < n; e0 += blockDim.x) {
@@ -74,12 +127,8 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps)
     uint32_t total = 0u, before = 0u;
     if (e < n) {
       if (counts != nullptr) {
-#pragma unroll 8
-        for (uint32_t c = 0; c < gridDim.x; ++c) {
-          const uint32_t v = counts[(size_t)c * n + e];
-          total += v;
-          before += c < blockIdx.x ? v : 0u;
-        }
+        total = all[e];
+        before = earlier[e];
       } else {
         for (uint32_t w = 0; w < warps; ++w) total += next[w * n + e];
       }
@@ -110,19 +159,24 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps)
     __syncthreads();
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) offsets[n] = (int64_t)slots;
-  for (uint32_t s0 = lo; s0 < hi; s0 += 32u) {
-    const uint32_t s = s0 + lane;
-    const bool in = s < hi;
-    const uint32_t e = in ? sort_key(ids, s, E) : n;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    if (in) {
-      const uint32_t r = mine[e] + __popc(same & ((1u << lane) - 1u));
-      rows[s] = e < E ? (int32_t)r : -1;
-      slot_of[r] = e < E ? (int32_t)s : -1;
+  const uint32_t bits = 32u - (uint32_t)__clz((int)n);
+  const bool once = hi - lo <= 128u;  // the keys are still here
+  for (uint32_t s0 = lo; s0 < hi; s0 += 128u) {
+    if (!once) sort_keys(ids, s0, hi, E, n, key);
+#pragma unroll
+    for (uint32_t i = 0; i < 4u; ++i) {
+      if (s0 + 32u * i >= hi) break;
+      const uint32_t s = s0 + 32u * i + lane, e = key[i];
+      const uint32_t same = same_key(e, bits);
+      if (e < n) {
+        const uint32_t r = mine[e] + __popc(same & ((1u << lane) - 1u));
+        rows[s] = e < E ? (int32_t)r : -1;
+        slot_of[r] = e < E ? (int32_t)s : -1;
+      }
+      __syncwarp();
+      if (e < n && lane == (uint32_t)__ffs((int)same) - 1u) mine[e] += __popc(same);
+      __syncwarp();
     }
-    __syncwarp();
-    if (in && lane == (uint32_t)__ffs((int)same) - 1u) mine[e] += __popc(same);
-    __syncwarp();
   }
 }
 
@@ -159,43 +213,44 @@ __global__ void __launch_bounds__(kThreads)
 // Back to token order: out[t] = sum_j weights[t, j] y[rows[t, j]] in fp32, in
 // the order of j, rounded once; weights == NULL sums with weight one (the
 // gradient of dispatch).
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     k_moe_combine(const V8* __restrict__ y, MoeShape sh, const int32_t* __restrict__ rows,
                   const float* __restrict__ weights, V8* __restrict__ out) {
+  constexpr uint32_t kBatch = 8u;  // rows on their way at a time
   pdl_begin();
   const uint32_t lane = threadIdx.x % 32u;
   const u64 units = (u64)sh.tokens * sh.segs;
   for (u64 u = (u64)blockIdx.x * (kThreads / 32) + threadIdx.x / 32u; u < units;
        u += (u64)gridDim.x * (kThreads / 32)) {
     const uint32_t t = (uint32_t)(u / sh.segs), w = (uint32_t)(u % sh.segs) * 32u + lane;
-    if (w >= sh.lanes) continue;
+    const bool in = w < sh.lanes;
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    for (uint32_t j0 = 0; j0 < sh.k; j0 += 4u) {
-      V8 v[4];
-      float f[4];
-      bool live[4];
+    for (uint32_t j0 = 0; j0 < sh.k; j0 += kBatch) {
+      // lane j reads the row number and weight of choice j0 + j for all
+      const uint32_t left = min(kBatch, sh.k - j0), s = t * sh.k + j0 + lane;
+      const int32_t my_row = lane < left ? rows[s] : -1;
+      const float my_f = weights == nullptr ? 1.0f : lane < left ? weights[s] : 0.0f;
+      V8 v[kBatch];
 #pragma unroll
-      for (uint32_t q = 0; q < 4u; ++q) {
-        const uint32_t s = t * sh.k + j0 + q;
-        const int32_t r = j0 + q < sh.k ? rows[s] : -1;
-        live[q] = (uint32_t)r < sh.slots;
-        if (live[q]) {
-          v[q] = ld_block_stream(y + (size_t)r * sh.lanes + w);
-          f[q] = weights != nullptr ? weights[s] : 1.0f;
-        }
+      for (uint32_t q = 0; q < kBatch; ++q) {
+        const uint32_t r = (uint32_t)__shfl_sync(0xFFFFFFFFu, my_row, q);
+        if (in && r < sh.slots) v[q] = ld_block_stream(y + (size_t)r * sh.lanes + w);
       }
 #pragma unroll
-      for (uint32_t q = 0; q < 4u; ++q) {
-        if (!live[q]) continue;
+      for (uint32_t q = 0; q < kBatch; ++q) {
+        const uint32_t r = (uint32_t)__shfl_sync(0xFFFFFFFFu, my_row, q);
+        const float f = __shfl_sync(0xFFFFFFFFu, my_f, q);
+        if (!(in && r < sh.slots)) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          acc[2 * i] = __fmaf_rn(f[q], bf16_lo(v[q].w[i]), acc[2 * i]);
-          acc[2 * i + 1] = __fmaf_rn(f[q], bf16_hi(v[q].w[i]), acc[2 * i + 1]);
+          acc[2 * i] = __fmaf_rn(f, bf16_lo(v[q].w[i]), acc[2 * i]);
+          acc[2 * i + 1] = __fmaf_rn(f, bf16_hi(v[q].w[i]), acc[2 * i + 1]);
         }
       }
     }
+    if (!in) continue;
     V8 o;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o.w[i] = cvt_bf16x2(acc[2 * i], acc[2 * i + 1]);

@@ -265,11 +265,26 @@ int coop_grid_for(const Shape& sh, int* grid) {
   return TRACE_OK;
 }
 
+// Slots per CTA of a sort (32-bit: slots + chunk stays below 2^32).
+uint32_t sort_chunk(uint64_t slots) {
+  const uint64_t c = (slots + kSortMaxChunks - 1) / kSortMaxChunks;
+  return c <= kSortChunk ? kSortChunk : (uint32_t)((c + 31) / 32 * 32);
+}
+
 template <typename ID>
 int moe_sort_launch(const ID* ids, uint32_t slots, uint32_t E, int64_t* offsets,
-                           int32_t* rows, int32_t* slot_of, uint32_t* counts, cudaStream_t s) {
-  const uint32_t chunks = (slots + kSortChunk - 1) / kSortChunk;
-  uint32_t warps = kSortSmem / (4u * (E + 1u));
+                    int32_t* rows, int32_t* slot_of, uint32_t* counts, cudaStream_t s) {
+  const uint32_t chunk = sort_chunk(slots), chunks = (slots + chunk - 1) / chunk;
+  uint32_t warps = kSortSmem / (4u * (E + 1u)) - 2u;
+  static bool attr_set[kMaxDevices];  // benign race: same value
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TRACE_ERR_CUDA;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(k_moe_place<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kSortSmem) != cudaSuccess)
+      return TRACE_ERR_CUDA;
+    attr_set[dev] = true;
+  }
   if (warps > (uint32_t)kSortMaxWarps) warps = kSortMaxWarps;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -282,12 +297,12 @@ int moe_sort_launch(const ID* ids, uint32_t slots, uint32_t E, int64_t* offsets,
   if (chunks > 1) {
     cfg.blockDim = dim3(512);
     cfg.dynamicSmemBytes = 4u * (E + 1u);
-    if (cudaLaunchKernelEx(&cfg, k_moe_count<ID>, ids, slots, E, counts) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, k_moe_count<ID>, ids, slots, chunk, E, counts) != cudaSuccess)
       return TRACE_ERR_CUDA;
   }
   cfg.blockDim = dim3(32u * warps);
-  cfg.dynamicSmemBytes = 4u * warps * (E + 1u);
-  return cudaLaunchKernelEx(&cfg, k_moe_place<ID>, ids, slots, E,
+  cfg.dynamicSmemBytes = 4u * (warps + 2u) * (E + 1u);
+  return cudaLaunchKernelEx(&cfg, k_moe_place<ID>, ids, slots, chunk, E,
                             (const uint32_t*)(chunks > 1 ? counts : nullptr), offsets, rows,
                             slot_of) == cudaSuccess
              ? TRACE_OK
@@ -1016,7 +1031,7 @@ static int check_slots(int64_t tokens, int64_t k) {
 
 size_t trace_moe_sort_workspace_bytes(int64_t tokens, int64_t k, int32_t num_experts) {
   if (check_slots(tokens, k) || num_experts < 1 || num_experts > TRACE_MOE_MAX_EXPERTS) return 0;
-  const uint64_t chunks = ((uint64_t)(tokens * k) + kSortChunk - 1) / kSortChunk;
+  const uint64_t n = (uint64_t)(tokens * k), chunk = sort_chunk(n), chunks = (n + chunk - 1) / chunk;
   const uint64_t words = chunks > 1 ? chunks * (uint64_t)(num_experts + 1) : 1;
   return (size_t)((words * 4 + 255) / 256 * 256);
 }
