@@ -15,6 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import dataclasses
+import functools
 import os
 import threading
 
@@ -753,6 +754,7 @@ class GuidedFakeQuant(torch.autograd.Function):
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class _On:
@@ -760,27 +762,27 @@ class _On:
     device's current stream), so that outputs are allocated there too; gives
     the stream's handle.  Nothing is switched in the common case, where the
     device is current and the stream is its own."""
-    __slots__ = ("dev", "stream", "undo")
+    __slots__ = ("index", "stream", "undo")
 
     def __init__(self, stream, *tensors):
-        dev = tensors[0].device
+        index = tensors[0].get_device()
         for t in tensors:
-            if t is not None and t.device != dev:
-                raise TraceError(f"tensors on different devices: {dev} and {t.device}")
-        if dev.type != "cuda":
+            if t is not None and t.get_device() != index:
+                raise TraceError(f"tensors on different devices: {tensors[0].device} and {t.device}")
+        if index < 0:
             raise TraceError("tensors passed to libtrace_fp4 must be CUDA tensors")
-        self.dev, self.stream, self.undo = dev, stream, None
+        self.index, self.stream, self.undo = index, stream, None
 
     def __enter__(self) -> int:
-        stream, index = self.stream, self.dev.index
-        if stream is None and index == torch.cuda.current_device():
+        stream, index = self.stream, self.index
+        if stream is None and index == _current_device():
             return _raw_stream(index)
         self.undo = contextlib.ExitStack()
-        self.undo.enter_context(torch.cuda.device(self.dev))
+        self.undo.enter_context(torch.cuda.device(index))
         if stream is None:
             return _raw_stream(index)
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.dev)
+            stream = torch.cuda.ExternalStream(int(stream), device=index)
         self.undo.enter_context(torch.cuda.stream(stream))
         return stream.cuda_stream
 
@@ -805,6 +807,7 @@ def _want(t: torch.Tensor, what: str, dtype, shape=None) -> None:
         raise TraceError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+@functools.lru_cache(maxsize=256)
 def trace_moe_sort_workspace_bytes(tokens: int, k: int, num_experts: int) -> int:
     return int(library().trace_moe_sort_workspace_bytes(tokens, k, num_experts))
 
@@ -828,7 +831,7 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, out: MoeRoute | None = 
     _want(expert_ids, "expert ids", (torch.int32, torch.int64))
     tokens, k = expert_ids.shape
     lib, base = library(), None
-    nbytes = lib.trace_moe_sort_workspace_bytes(tokens, k, num_experts)
+    nbytes = trace_moe_sort_workspace_bytes(tokens, k, num_experts)
     if nbytes == 0:
         raise TraceError(f"moe_sort: {num_experts} experts for [{tokens}, {k}] ids")
     with _On(stream, expert_ids, workspace) as s:
@@ -940,6 +943,7 @@ class MoeDispatch(torch.autograd.Function):
         return moe_dispatch_fwd(x, route)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         return moe_dispatch_bwd(grad.contiguous(), MoeRoute(*ctx.saved_tensors)), None
 
@@ -953,6 +957,7 @@ class MoeCombine(torch.autograd.Function):
         return moe_combine_fwd(y, route, weights)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         y, weights, *route = ctx.saved_tensors
         grad_y, grad_w = moe_combine_bwd(grad.contiguous(), y, MoeRoute(*route), weights)

@@ -468,3 +468,120 @@ def test_training_layer_gradients():
     mag = np.where(live[..., None], dqm[np.maximum(rows, 0)], 0.0).sum(1)
     # dy (2^-8), the product's rounding (2^-8) and the sum's (2^-8), each of the magnitudes
     assert np.all(np.abs(ref.f64(dx) - want) <= 3.1 * 2.0 ** -8 * mag)
+
+
+# ---------------------------------------------------------------------------
+# Products whose tiles two CTAs share (large groups, tiled scales), and
+# products whose k several CTAs share (few tiles)
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,n,cols", [
+    (129, 129, 64), (192, 130, 192), (255, 256, 320), (256, 257, 448), (257, 384, 704),
+    (384, 1000, 128), (449, 392, 512), (600, 133, 832), (1025, 264, 1024), (3000, 520, 256)])
+def test_product_of_pairs(fmt, rows, n, cols):
+    """Ends of tokens, of columns and of k (a last stage of 64, 128 or 192
+    elements) inside a tile; rows of out with and without 16-byte alignment."""
+    _product_case(rows, n, cols, fmt, True, True, seed=rows + n)
+
+
+PAIR_GROUPS = [
+    [300, 2, 400], [129, 256, 1, 0, 700], [0, 600, 0, 3], [63, 500, 65, 191], [64, 64, 640],
+    [257, 255, 320], [1000], [100, 700, None], [0, 0, 900, None], [127, 1, 385, 64, 300]]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("counts", PAIR_GROUPS, ids=str)
+@pytest.mark.parametrize("n,cols", [(256, 320), (384, 512), (640, 64)])
+def test_grouped_product_of_pairs(fmt, counts, n, cols):
+    """Groups that start at any row of a 128-row block: in its first or second
+    half, with more or fewer than 64 rows of another group before it."""
+    rows = sum(c for c in counts if c is not None) + (333 if counts[-1] is None else 0)
+    groups = len(counts)
+    assert -(-rows // groups) > 128 and n % 128 == 0  # the rule that picks pairs
+    _product_case(rows, n, cols, fmt, True, True, counts, seed=len(counts) + rows)
+
+
+def test_rows_around_the_groups_of_pairs_are_left():
+    rows, n, cols = 900, 256, 128
+    a = inputs.tiny_site(1, rows, cols).x_roll.to(DEV)
+    w = inputs.tiny_site(2, 2 * n, cols).x_roll.to(DEV)
+    bounds = torch.arange(3, dtype=torch.int64, device=DEV) * n
+    cw = ops.capture_tiled(w, bounds)
+    ca = ops.capture_tiled(a, torch.tensor([0, 450, 900], dtype=torch.int64, device=DEV))
+    whole = ops.fp4_matmul(ca, cw, cols)
+    out = torch.full((rows, n), 5.0, dtype=torch.bfloat16, device=DEV)
+    ca.offsets = torch.tensor([101, 450, 700], dtype=torch.int64, device=DEV)
+    ops.fp4_matmul(ca, cw, cols, out=out)
+    assert torch.equal(out[101:700], whole[101:700])
+    assert bool((out[:101] == 5.0).all()) and bool((out[700:] == 5.0).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,n,cols", [
+    (1, 128, 512), (5, 129, 1024), (16, 8, 544), (31, 2048, 768), (100, 4096, 1056),
+    (128, 256, 4096), (190, 100, 2048), (700, 128, 1568)])
+def test_product_with_k_split(fmt, rows, n, cols):
+    _product_case(rows, n, cols, fmt, True, cols % 64 == 0, seed=rows + n)
+
+
+def test_product_on_two_streams_and_in_graphs():
+    """Two captured graphs of pair and split products replayed at once on two
+    streams, and products interleaved with them: nothing is shared."""
+    cases = []
+    for i, (rows, n, cols) in enumerate([(900, 512, 1024), (8, 512, 2048)]):
+        a = ops.capture_tiled(inputs.tiny_site(2 * i, rows, cols).x_roll.to(DEV))
+        w = ops.capture_tiled(inputs.tiny_site(2 * i + 1, n, cols).x_roll.to(DEV))
+        cases.append((a, w, cols, ops.fp4_matmul(a, w, cols)))
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs = [ops.fp4_matmul(a, w, cols) for a, w, cols, _ in cases * 3]
+        graphs.append((s, g, outs))
+    for _ in range(5):
+        for s, g, outs in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+        extra = [ops.fp4_matmul(a, w, cols) for a, w, cols, _ in cases]
+    torch.cuda.synchronize()
+    for outs in [o for _, _, o in graphs] + [extra]:
+        for i, o in enumerate(outs):
+            assert torch.equal(o, cases[i % 2][3])
+    assert ops.matmul_status()
+
+
+@pytest.mark.parametrize("tokens,k,experts", [(300000, 8, 5), (140000, 8, 64), (1100, 4, 4096)])
+def test_sort_of_many_slots(tokens, k, experts):
+    """More slots than the most chunks of the usual size; more experts than a
+    CTA has threads."""
+    g = _gen(tokens)
+    ids = torch.randint(-1, experts, (tokens, k), generator=g).to(torch.int32)
+    route = ops.moe_sort(ids.to(DEV), experts)
+    key = torch.where(ids >= 0, ids, experts).reshape(-1)
+    order = torch.sort(key, stable=True).indices
+    want = torch.where(key[order] < experts, order, -1).to(torch.int32)
+    assert torch.equal(route.slots.cpu(), want)
+    rows = torch.empty_like(order)
+    rows[order] = torch.arange(order.numel())
+    rows = torch.where(key < experts, rows, -1).to(torch.int32).view(tokens, k)
+    assert torch.equal(route.rows.cpu(), rows)
+    counts = torch.bincount(key, minlength=experts + 1)
+    assert route.offsets.cpu().tolist() == [0] + torch.cumsum(counts, 0).tolist()
+
+
+@pytest.mark.parametrize("k", [1, 7, 8, 9, 40])
+def test_combine_of_many_choices(k):
+    """Choices beyond one batch of rows, and rows that are no multiple of a warp's."""
+    tokens, experts, cols = 21, 6, 1056
+    route, (_, rows, _) = _route(tokens, k, experts, k, dropped=0.2)
+    g = _gen(k)
+    y = torch.randn(tokens * k, cols, generator=g).bfloat16().to(DEV)
+    w = torch.randn(tokens, k, generator=g).to(DEV)
+    out = ref.f64(ops.moe_combine(y, route, w))
+    terms = np.where((rows >= 0)[..., None], ref.f64(y)[np.maximum(rows, 0)], 0.0) \
+        * ref.f64(w)[..., None]
+    s, m = terms.sum(1), np.abs(terms).sum(1)
+    # one rounding to bf16 of a sum of k fused steps in fp32
+    assert np.all(np.abs(out - s) <= 2.0 ** -8 * np.abs(s) + (1 + 2.0 ** -8) * k * 2.0 ** -24 * m)
