@@ -49,6 +49,7 @@ struct MmShape {
   int32_t groups, matrices;
   uint32_t nt;                 // tokens of a full tile (multiple of 16)
   uint32_t n_tiles;            // ceil(n / 128), of pairs ceil(n / 256)
+  uint32_t w_blocks;           // ceil(n / 128): of pairs, a matrix's 128-row blocks of scales
   uint32_t ksteps;             // stages of a whole product
   uint32_t stages, accs, sf_slots;
   uint32_t step_tokens, step_j;  // token and w tiles from one of a CTA's (a team's) to its next
@@ -632,7 +633,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         // blocks of 128 rows that the tile's scales lie in
         const uint32_t width = mm_width<CG>(m.tokens);
         const bool two = (uint32_t)(m.row0 % 128) + width > 128u;
-        const int32_t wb = w_row / 128, row = (int32_t)uniform((uint32_t)m.row0), xb = row / 128;
+        const int32_t wb = (int32_t)uniform((uint32_t)m.group * sh.w_blocks + (m.j0 + j_rank) / 128u);
+        const int32_t row = (int32_t)uniform((uint32_t)m.row0), xb = row / 128;
         const int32_t xr = row + (int32_t)uniform(rank * (width / 2u));
         const uint32_t bytes = 2u * (w_code + x_code + (two ? 3u : 2u) * block_bytes);
         for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages)) {
@@ -912,5 +914,68 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     else
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                    "r"(kMmTmemCols));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Scales for pairs from a layout that the copy engine cannot take: row-major,
+// or tiled with matrices that do not begin at a 128-row block or rows of scales
+// that end inside a piece of four columns.  To the 128 x 4 tiled layout, each
+// matrix from a block of its own, zeros past the last row and column.  A CTA
+// takes 128 rows x 16 pieces, 64 bytes of a row at a time.  Bound by the launch
+// and one latency of memory (operands of 16384 x 2048 and 4096 x 2048: 5 of
+// 74 us with the product, which takes 179 us on the rows as they are).
+// ---------------------------------------------------------------------------
+struct RetileSrc {
+  const uint8_t* src;
+  uint8_t* dst;
+  int64_t rows;      // of a matrix
+  uint32_t blocks;   // 128-row blocks of a matrix
+  uint32_t ctas;     // of all matrices: 0 if the operand stays as it is
+  uint8_t tiled, bytes;
+};
+
+__global__ void __launch_bounds__(kThreads)
+    k_retile_scales(RetileSrc a, RetileSrc w, uint32_t scols) {
+  __shared__ uint32_t words[16 * 128];
+  pdl_begin();
+  const bool first = blockIdx.x < a.ctas;
+  const RetileSrc& s = first ? a : w;
+  const uint32_t cta = first ? blockIdx.x : blockIdx.x - a.ctas;
+  const uint32_t pieces = (scols + 3u) / 4u, runs = (pieces + 15u) / 16u;
+  const uint32_t block = cta / runs, p0 = (cta - block * runs) * 16u;
+  const uint32_t matrix = block / s.blocks;
+  const int64_t r0 = (int64_t)(block - matrix * s.blocks) * 128;  // in its matrix
+  uint32_t v[8], keep[8], to[8];
+#pragma unroll
+  for (uint32_t i = 0; i < 8u; ++i) {  // eight loads on their way at once
+    // neighbours along a row, or in the tiled order
+    const uint32_t x = threadIdx.x + kThreads * i;
+    const uint32_t p = s.tiled ? x / 128u : x % 16u;
+    const uint32_t r = s.tiled ? x % 4u * 32u + x % 128u / 4u : x / 16u, c = 4u * (p0 + p);
+    const uint32_t take = r0 + r < s.rows && c < scols ? min(4u, scols - c) : 0u;
+    const u64 row = (u64)(matrix * s.rows + r0) + r;
+    const u64 at = take == 0u ? 0u
+                   : s.tiled  ? ((row / 128u) * pieces + p0 + p) * 512u + row % 32u * 16u +
+                                   row % 128u / 32u * 4u
+                              : row * scols + c;
+    to[i] = p * 128u + r % 32u * 4u + r / 32u;
+    keep[i] = take == 4u ? 0xFFFFFFFFu : (1u << (8u * take)) - 1u;
+    if (!s.bytes) {
+      v[i] = *reinterpret_cast<const uint32_t*>(s.src + at);
+    } else {
+      v[i] = 0u;
+      for (uint32_t b = 0; b < take; ++b) v[i] |= (uint32_t)s.src[at + b] << (8u * b);
+    }
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < 8u; ++i) words[to[i]] = v[i] & keep[i];
+  __syncthreads();
+#pragma unroll
+  for (uint32_t i = 0; i < 2u; ++i) {
+    const uint32_t x = threadIdx.x + kThreads * i;  // 16 bytes each
+    if (p0 + x / 32u < pieces)
+      *reinterpret_cast<uint4*>(s.dst + ((size_t)block * pieces + p0) * 512u + 16u * x) =
+          *reinterpret_cast<const uint4*>(words + 4u * x);
   }
 }

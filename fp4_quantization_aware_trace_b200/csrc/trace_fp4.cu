@@ -362,11 +362,46 @@ int scale_map(CUtensorMap* map, const uint8_t* scales, uint64_t rows, uint32_t s
              : TRACE_ERR_CUDA;
 }
 
+// What a product does with its scales.
+struct MmPlan {
+  int64_t mean;           // rows of a group
+  bool pairs;             // two CTAs to a tile (if a workspace is there where it is needed)
+  bool retile_a, retile_w;  // the copy engine cannot take the scales as they are
+  uint64_t a_bytes, w_bytes;  // of the retiled scales
+};
+
+MmPlan matmul_plan(bool mx, int64_t rows, int64_t cols, int32_t groups, int a_layout, int64_t n,
+                   int32_t matrices, int w_layout) {
+  MmPlan p;
+  p.mean = (rows + groups - 1) / groups;
+  // whole 64s of k: a piece of four scale columns that ended inside a product
+  // would bring its padding; matrices of whole 128-row blocks
+  const bool whole = cols % 64 == 0;
+  p.retile_a = !(a_layout == TRACE_SCALES_TILED_128x4 && whole);
+  p.retile_w = !(w_layout == TRACE_SCALES_TILED_128x4 && whole && (matrices == 1 || n % kMmM == 0));
+  // Pairs where tiles are large; if scales have to be copied first (4 to 6 us),
+  // where that pays: NVFP4 rows, which single CTAs read 4 bytes at a time
+  // (2048 x 4096 x 4096: 24.9 us copied, 56.1 as they are; 512 x 1024 x 1024:
+  // 9.6 and 10.1), and the rest from 2^33 products on (MXFP4 rows, 2048^3: 12.7
+  // and 14.6, 1024 x 2048 x 2048: 11.6 and 9.7; NVFP4 tiled, 4 matrices of 1000:
+  // 4096 x 1000 x 4096 20.6 and 22.9, 4096 x 1000 x 1024 14.9 and 11.6).
+  const bool rows_nv = !mx && !(a_layout == TRACE_SCALES_TILED_128x4 &&
+                                w_layout == TRACE_SCALES_TILED_128x4);
+  const bool pays = !(p.retile_a || p.retile_w) || rows_nv ||
+                    (long double)rows * n * cols >= 8589934592.0L;
+  p.pairs = p.mean > 128 && n > kMmM && pays;
+  const uint64_t pieces = (uint64_t)(cols / (mx ? 32 : 16) + 3) / 4;
+  p.a_bytes = p.retile_a ? (uint64_t)((rows + 127) / 128) * pieces * 512u : 0;
+  p.w_bytes = p.retile_w ? (uint64_t)((n + 127) / 128) * matrices * pieces * 512u : 0;
+  return p;
+}
+
 template <bool MX>
 int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gscale,
                   int64_t rows, int64_t cols, int32_t groups, const int64_t* offs, int a_layout,
                   const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gscale,
-                  int64_t n, int32_t matrices, int w_layout, uint16_t* out, cudaStream_t stream) {
+                  int64_t n, int32_t matrices, int w_layout, uint16_t* out, uint8_t* ws,
+                  cudaStream_t stream) {
   constexpr uint32_t kAtoms = MX ? 2 : 4;
   constexpr uint32_t kSmem = 227u * 1024u;
   const int sms = sm_count();
@@ -378,15 +413,32 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   sh.scols = (uint32_t)(cols / (MX ? 32 : 16));
   sh.groups = groups;
   sh.matrices = matrices;
-  const int64_t mean = (rows + groups - 1) / groups;
-  sh.nt = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : kMmTokens;
+  const MmPlan plan = matmul_plan(MX, rows, cols, groups, a_layout, n, matrices, w_layout);
+  sh.nt = plan.mean <= 16    ? 16
+          : plan.mean <= 32  ? 32
+          : plan.mean <= 64  ? 64
+          : plan.mean <= 128 ? 128
+                             : kMmTokens;
   sh.a_tiled = a_layout == TRACE_SCALES_TILED_128x4;
   sh.w_tiled = w_layout == TRACE_SCALES_TILED_128x4;
-  // Two CTAs to a tile where tiles are large and the copy engine can take every
-  // scale: tiled layouts, whole 64s of k (a piece of four scale columns that
-  // ends inside a product would bring its padding), matrices of whole blocks.
-  const bool pair = mean > 128 && n > kMmM && sh.a_tiled && sh.w_tiled && cols % 64 == 0 &&
-                    (matrices == 1 || n % kMmM == 0);
+  sh.a_bytes = !sh.a_tiled && (sh.scols % 4 != 0 || !aligned(a_scales, 4));
+  sh.w_bytes = !sh.w_tiled && (sh.scols % 4 != 0 || !aligned(w_scales, 4));
+  sh.w_blocks = (uint32_t)((n + 127) / 128);
+  const bool pair = plan.pairs && (ws != nullptr || (!plan.retile_a && !plan.retile_w));
+  if (pair && (plan.retile_a || plan.retile_w)) {
+    const uint64_t runs = ((sh.scols + 3u) / 4u + 15u) / 16u;
+    RetileSrc a{a_scales, ws, rows, (uint32_t)((rows + 127) / 128), 0, sh.a_tiled, sh.a_bytes};
+    RetileSrc w{w_scales, ws + plan.a_bytes, n, sh.w_blocks, 0, sh.w_tiled, sh.w_bytes};
+    const uint64_t a_ctas = plan.retile_a ? a.blocks * runs : 0;
+    const uint64_t w_ctas = plan.retile_w ? (uint64_t)w.blocks * matrices * runs : 0;
+    if (a_ctas + w_ctas > 0x7FFFFFFFu) return TRACE_ERR_SHAPE;
+    a.ctas = (uint32_t)a_ctas;
+    w.ctas = (uint32_t)w_ctas;
+    const int st = launch(k_retile_scales, (int)(a_ctas + w_ctas), stream, a, w, sh.scols);
+    if (st) return st;
+    if (plan.retile_a) a_scales = a.dst;
+    if (plan.retile_w) w_scales = w.dst;
+  }
   const uint32_t cg = pair ? 2 : 1;
   if (pair) sh.nt = kMmPairTokens;
   sh.n_tiles = (uint32_t)((n + cg * kMmM - 1) / (cg * kMmM));
@@ -408,14 +460,12 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   if (groups == 1 && !pair)
     while (sh.split < kMmMaxSplit && tiles * (sh.split * 2) <= 128 && sh.ksteps >= sh.split * 2)
       sh.split *= 2;
-  sh.a_bytes = !sh.a_tiled && (sh.scols % 4 != 0 || !aligned(a_scales, 4));
-  sh.w_bytes = !sh.w_tiled && (sh.scols % 4 != 0 || !aligned(w_scales, 4));
   sh.out16 = n % 8 == 0;
   MmMaps maps;
   int st = code_map(&maps.a, a_codes, (uint64_t)rows, (uint64_t)cols / 2, sh.nt / cg);
   if (!st) st = code_map(&maps.w, w_codes, (uint64_t)n * matrices, (uint64_t)cols / 2, kMmM);
   if (!st && pair) st = scale_map(&maps.as, a_scales, (uint64_t)rows, sh.scols, kAtoms);
-  if (!st && pair) st = scale_map(&maps.ws, w_scales, (uint64_t)n * matrices, sh.scols, kAtoms);
+  if (!st && pair) st = scale_map(&maps.ws, w_scales, (uint64_t)sh.w_blocks * matrices * 128u, sh.scols, kAtoms);
   if (st) return st;
   static bool attr_set[kMaxDevices];  // benign race: same value
   int dev = 0;
@@ -1125,19 +1175,36 @@ int trace_moe_combine_bwd(const uint16_t* grad_out, const uint16_t* y, int64_t t
                 sh, rows, slots, weights, (V8*)grad_y, grad_weights);
 }
 
-static int matmul_impl(bool mx, const uint8_t* a_codes, const uint8_t* a_scales,
-                       const float* a_gscale, int64_t rows, int64_t cols, int32_t num_groups,
-                       const int64_t* offs, int32_t a_layout, const uint8_t* w_codes,
-                       const uint8_t* w_scales, const float* w_gscale, int64_t n,
-                       int32_t num_matrices, int32_t w_layout, uint16_t* out, void* stream) {
-  int st = check_shape(rows, cols, num_groups, offs);
-  if (st) return st;
+static int matmul_shape(int64_t rows, int64_t cols, int32_t num_groups, int32_t a_layout, int64_t n,
+                        int32_t num_matrices, int32_t w_layout) {
   if (n < 1 || num_matrices < 1 || num_groups > TRACE_MATMUL_MAX_GROUPS ||
       num_matrices > num_groups || !valid_layout(a_layout) || !valid_layout(w_layout) ||
       rows > ((int64_t)1 << 31) - 512 || n * (long double)num_matrices > 2147483136.0L ||
       cols > ((int64_t)1 << 31) - 512)
     return TRACE_ERR_SHAPE;
-  if ((st = check_shape(n * num_matrices, cols, 1, nullptr))) return st;
+  return check_shape(n * num_matrices, cols, 1, nullptr);
+}
+
+static size_t matmul_workspace(bool mx, int64_t rows, int64_t cols, int32_t num_groups,
+                               int32_t a_layout, int64_t n, int32_t num_matrices,
+                               int32_t w_layout) {
+  static const int64_t some = 0;  // offsets are not read here
+  if (check_shape(rows, cols, num_groups, &some) ||
+      matmul_shape(rows, cols, num_groups, a_layout, n, num_matrices, w_layout))
+    return 0;
+  const MmPlan p = matmul_plan(mx, rows, cols, num_groups, a_layout, n, num_matrices, w_layout);
+  return p.pairs ? (size_t)(p.a_bytes + p.w_bytes) : 0;
+}
+
+static int matmul_impl(bool mx, const uint8_t* a_codes, const uint8_t* a_scales,
+                       const float* a_gscale, int64_t rows, int64_t cols, int32_t num_groups,
+                       const int64_t* offs, int32_t a_layout, const uint8_t* w_codes,
+                       const uint8_t* w_scales, const float* w_gscale, int64_t n,
+                       int32_t num_matrices, int32_t w_layout, uint16_t* out, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  int st = check_shape(rows, cols, num_groups, offs);
+  if (!st) st = matmul_shape(rows, cols, num_groups, a_layout, n, num_matrices, w_layout);
+  if (st) return st;
   if (rows == 0) return TRACE_OK;
   if (!a_codes || !a_scales || !w_codes || !w_scales || !out ||
       (!mx && (!a_gscale || !w_gscale)))
@@ -1145,14 +1212,20 @@ static int matmul_impl(bool mx, const uint8_t* a_codes, const uint8_t* a_scales,
   // tiled scales are read in 16-byte pieces
   if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(out, 16) ||
       (a_layout && !aligned(a_scales, 16)) || (w_layout && !aligned(w_scales, 16)) ||
-      !aligned(a_gscale, 4) || !aligned(w_gscale, 4) || !aligned(offs, 8))
+      !aligned(a_gscale, 4) || !aligned(w_gscale, 4) || !aligned(offs, 8) ||
+      !aligned(workspace, 256))
     return TRACE_ERR_ALIGN;
+  if (workspace != nullptr &&
+      workspace_bytes <
+          matmul_workspace(mx, rows, cols, num_groups, a_layout, n, num_matrices, w_layout))
+    return TRACE_ERR_WORKSPACE;
+  uint8_t* ws = (uint8_t*)workspace;
   return mx ? matmul_launch<true>(a_codes, a_scales, nullptr, rows, cols, num_groups, offs,
                                   a_layout, w_codes, w_scales, nullptr, n, num_matrices, w_layout,
-                                  out, (cudaStream_t)stream)
+                                  out, ws, (cudaStream_t)stream)
             : matmul_launch<false>(a_codes, a_scales, a_gscale, rows, cols, num_groups, offs,
                                    a_layout, w_codes, w_scales, w_gscale, n, num_matrices,
-                                   w_layout, out, (cudaStream_t)stream);
+                                   w_layout, out, ws, (cudaStream_t)stream);
 }
 
 int trace_fp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gscale,
@@ -1163,7 +1236,32 @@ int trace_fp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const floa
                      void* stream) {
   return matmul_impl(false, a_codes, a_scales, a_gscale, rows, cols, num_groups,
                      group_row_offsets, a_scale_layout, w_codes, w_scales, w_gscale, n,
-                     num_matrices, w_scale_layout, out, stream);
+                     num_matrices, w_scale_layout, out, nullptr, 0, stream);
+}
+
+int trace_fp4_matmul_ws(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gscale,
+                        int64_t rows, int64_t cols, int32_t num_groups,
+                        const int64_t* group_row_offsets, int32_t a_scale_layout,
+                        const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gscale,
+                        int64_t n, int32_t num_matrices, int32_t w_scale_layout, uint16_t* out,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  return matmul_impl(false, a_codes, a_scales, a_gscale, rows, cols, num_groups,
+                     group_row_offsets, a_scale_layout, w_codes, w_scales, w_gscale, n,
+                     num_matrices, w_scale_layout, out, workspace, workspace_bytes, stream);
+}
+
+size_t trace_fp4_matmul_workspace_bytes(int64_t rows, int64_t cols, int32_t num_groups,
+                                        int32_t a_scale_layout, int64_t n, int32_t num_matrices,
+                                        int32_t w_scale_layout) {
+  return matmul_workspace(false, rows, cols, num_groups, a_scale_layout, n, num_matrices,
+                          w_scale_layout);
+}
+
+size_t trace_mx_matmul_workspace_bytes(int64_t rows, int64_t cols, int32_t num_groups,
+                                       int32_t a_scale_layout, int64_t n, int32_t num_matrices,
+                                       int32_t w_scale_layout) {
+  return matmul_workspace(true, rows, cols, num_groups, a_scale_layout, n, num_matrices,
+                          w_scale_layout);
 }
 
 int trace_matmul_status(void* stream) {
@@ -1188,7 +1286,17 @@ int trace_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t row
                     int32_t num_matrices, int32_t w_scale_layout, uint16_t* out, void* stream) {
   return matmul_impl(true, a_codes, a_scales, nullptr, rows, cols, num_groups, group_row_offsets,
                      a_scale_layout, w_codes, w_scales, nullptr, n, num_matrices, w_scale_layout,
-                     out, stream);
+                     out, nullptr, 0, stream);
+}
+
+int trace_mx_matmul_ws(const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows, int64_t cols,
+                       int32_t num_groups, const int64_t* group_row_offsets,
+                       int32_t a_scale_layout, const uint8_t* w_codes, const uint8_t* w_scales,
+                       int64_t n, int32_t num_matrices, int32_t w_scale_layout, uint16_t* out,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  return matmul_impl(true, a_codes, a_scales, nullptr, rows, cols, num_groups, group_row_offsets,
+                     a_scale_layout, w_codes, w_scales, nullptr, n, num_matrices, w_scale_layout,
+                     out, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -131,6 +131,15 @@ def library() -> ctypes.CDLL:
         lib.trace_fp4_matmul.restype = ctypes.c_int
         lib.trace_mx_matmul.argtypes = [P, P, i64, i64, i32, P, i32, P, P, i64, i32, i32, P, P]
         lib.trace_mx_matmul.restype = ctypes.c_int
+        lib.trace_fp4_matmul_ws.argtypes = [P, P, P, i64, i64, i32, P, i32, P, P, P, i64, i32, i32,
+                                            P, P, sz, P]
+        lib.trace_fp4_matmul_ws.restype = ctypes.c_int
+        lib.trace_mx_matmul_ws.argtypes = [P, P, i64, i64, i32, P, i32, P, P, i64, i32, i32, P, P,
+                                           sz, P]
+        lib.trace_mx_matmul_ws.restype = ctypes.c_int
+        for f in (lib.trace_fp4_matmul_workspace_bytes, lib.trace_mx_matmul_workspace_bytes):
+            f.argtypes = [i64, i64, i32, i32, i64, i32, i32]
+            f.restype = sz
         lib.trace_matmul_status.argtypes = [P]
         lib.trace_matmul_status.restype = ctypes.c_int
         lib.trace_capture_status.argtypes = [P, P]
@@ -998,7 +1007,16 @@ def _matmul_operand(cap, cols: int, bs: int, what: str) -> tuple[int, int]:
     return rows, layout
 
 
-def _matmul(a, w, cols, offsets, matrices, out, stream, bs):
+@functools.lru_cache(maxsize=256)
+def trace_matmul_workspace_bytes(mx: bool, rows: int, cols: int, num_groups: int,
+                                 a_scale_layout: int, n: int, num_matrices: int,
+                                 w_scale_layout: int) -> int:
+    lib = library()
+    f = lib.trace_mx_matmul_workspace_bytes if mx else lib.trace_fp4_matmul_workspace_bytes
+    return int(f(rows, cols, num_groups, a_scale_layout, n, num_matrices, w_scale_layout))
+
+
+def _matmul(a, w, cols, offsets, matrices, out, workspace, stream, bs):
     if cols is None:
         s = next((c.scales for c in (a, w) if c.scales.dim() == 2), None)
         if s is None:
@@ -1013,46 +1031,55 @@ def _matmul(a, w, cols, offsets, matrices, out, stream, bs):
         raise TraceError(f"w: {wrows} rows are no {matrices} matrices")
     n = wrows // matrices
     ga, gw = (a.gscale, w.gscale) if bs == 16 else (None, None)
-    with _On(stream, a.codes, a.scales, w.codes, w.scales, offsets, ga, gw, out) as s:
+    with _On(stream, a.codes, a.scales, w.codes, w.scales, offsets, ga, gw, out, workspace) as s:
         if out is None:
             out = a.codes.new_empty((rows, n), dtype=torch.bfloat16)
         else:
             _want(out, "out", torch.bfloat16, (rows, n))
-        ac, asc, wc, wsc, po, pf = _ptrs(a.codes, a.scales, w.codes, w.scales, out, offsets)
+        if workspace is None:
+            nbytes = trace_matmul_workspace_bytes(bs == 32, rows, cols, groups, la, n, matrices, lw)
+            workspace = a.codes.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+        else:
+            nbytes = workspace.numel() * workspace.element_size()
+        ac, asc, wc, wsc, po, pf, pws = _ptrs(a.codes, a.scales, w.codes, w.scales, out, offsets,
+                                              workspace)
         if bs == 16:
             _want(ga, "a global scales", torch.float32, (groups,))
             _want(gw, "w global scales", torch.float32, (matrices,))
             pa, pw = _ptrs(ga, gw)
-            st = library().trace_fp4_matmul(ac, asc, pa, rows, cols, groups, pf, la, wc, wsc, pw, n,
-                                            matrices, lw, po, s)
+            st = library().trace_fp4_matmul_ws(ac, asc, pa, rows, cols, groups, pf, la, wc, wsc, pw,
+                                               n, matrices, lw, po, pws, nbytes, s)
         else:
-            st = library().trace_mx_matmul(ac, asc, rows, cols, groups, pf, la, wc, wsc, n, matrices,
-                                           lw, po, s)
+            st = library().trace_mx_matmul_ws(ac, asc, rows, cols, groups, pf, la, wc, wsc, n,
+                                              matrices, lw, po, pws, nbytes, s)
         _check(st, "trace_fp4_matmul" if bs == 16 else "trace_mx_matmul")
     return out
 
 
 def fp4_matmul(a: Capture, w: Capture, cols: int | None = None, out: torch.Tensor | None = None,
-               stream=None) -> torch.Tensor:
+               stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Product of two NVFP4 captures, bf16 [rows, n]: a of [rows, cols], w of
     one matrix [n, cols], or of one per expert stacked by rows (w.gscale has
     one entry per matrix, a.offsets groups the rows).  Rows of a's groups
     behind w's matrices (dropped slots) become zero.  cols is needed when
-    both scales are tiled.  Has no gradient: codes are the rollout's; the
+    both scales are tiled.  Large products copy scales that are not tiled
+    into `workspace` (trace_matmul_workspace_bytes; allocated if None).  Has
+    no gradient: codes are the rollout's; the
     training side differentiates through trace_fake_quant."""
     if not isinstance(a, Capture) or not isinstance(w, Capture):
         raise TraceError("fp4_matmul takes two NVFP4 captures")
-    return _matmul(a, w, cols, a.offsets, w.gscale.numel(), out, stream, 16)
+    return _matmul(a, w, cols, a.offsets, w.gscale.numel(), out, workspace, stream, 16)
 
 
 def mx_matmul(a: MxCapture, w: MxCapture, cols: int | None = None,
               offsets: torch.Tensor | None = None, groups: int = 1,
-              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+              out: torch.Tensor | None = None, stream=None,
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Product of two MXFP4 captures, bf16 [rows, n]; grouped when `offsets`
     (int64 row bounds of a) and `groups` (matrices stacked in w) are given."""
     if not isinstance(a, MxCapture) or not isinstance(w, MxCapture):
         raise TraceError("mx_matmul takes two MXFP4 captures")
-    return _matmul(a, w, cols, offsets, groups, out, stream, 32)
+    return _matmul(a, w, cols, offsets, groups, out, workspace, stream, 32)
 
 
 def matmul_status(stream=None) -> bool:

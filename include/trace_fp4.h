@@ -555,6 +555,32 @@ int trace_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t row
                     const uint8_t* w_codes, const uint8_t* w_scales, int64_t n,
                     int32_t num_matrices, int32_t w_scale_layout, uint16_t* out, void* stream);
 
+/* The same with a workspace: at least trace_*_matmul_workspace_bytes() bytes,
+ * 256-byte aligned, contents of no account before and after, not shared by
+ * calls that may run at the same time.  The fastest form of a large product
+ * (more than 128 rows to a group on average, n > 128) takes scales in the
+ * 128 x 4 tiled layout, with cols a multiple of 64 and, of several matrices, n
+ * a multiple of 128.  Where it pays, scales that are not like that are first
+ * copied there; the query is 0 where nothing is copied (or the shape is
+ * refused), and NULL runs the product on the scales as they are. */
+size_t trace_fp4_matmul_workspace_bytes(int64_t rows, int64_t cols, int32_t num_groups,
+                                        int32_t a_scale_layout, int64_t n, int32_t num_matrices,
+                                        int32_t w_scale_layout);
+int trace_fp4_matmul_ws(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gscale,
+                        int64_t rows, int64_t cols, int32_t num_groups,
+                        const int64_t* group_row_offsets, int32_t a_scale_layout,
+                        const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gscale,
+                        int64_t n, int32_t num_matrices, int32_t w_scale_layout, uint16_t* out,
+                        void* workspace, size_t workspace_bytes, void* stream);
+size_t trace_mx_matmul_workspace_bytes(int64_t rows, int64_t cols, int32_t num_groups,
+                                       int32_t a_scale_layout, int64_t n, int32_t num_matrices,
+                                       int32_t w_scale_layout);
+int trace_mx_matmul_ws(const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows, int64_t cols,
+                       int32_t num_groups, const int64_t* group_row_offsets,
+                       int32_t a_scale_layout, const uint8_t* w_codes, const uint8_t* w_scales,
+                       int64_t n, int32_t num_matrices, int32_t w_scale_layout, uint16_t* out,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
 /* Whether a product on the current device has given up a wait for its own
  * copies since the last check (every wait is bounded; none is expected to
  * run out): waits for the work queued on `stream`, reads and clears one word

@@ -105,3 +105,27 @@ def test_binding_refusals(lib):
                  lambda: ops.moe_combine(y, route, w.double()), lambda: ops.moe_combine(y, route, w)):
         with pytest.raises(ops.TraceError):
             call()
+
+
+def test_product_workspace(lib):
+    """Bytes of the tiled copies: 512 for 128 rows x 4 scale columns."""
+    nv, mx = lib.trace_fp4_matmul_workspace_bytes, lib.trace_mx_matmul_workspace_bytes
+    assert nv(2048, 4096, 1, 1, 4096, 1, 1) == 0                     # both tiled
+    assert nv(2048, 4096, 1, 0, 4096, 1, 1) == 16 * 64 * 512
+    assert nv(2048, 4096, 1, 1, 4096, 1, 0) == 32 * 64 * 512
+    assert nv(2049, 4128, 1, 0, 4097, 1, 0) == (17 + 33) * 65 * 512
+    assert nv(2048, 4128, 1, 1, 4096, 1, 1) == (16 + 32) * 65 * 512  # k ends inside a piece
+    assert nv(4096, 4096, 4, 1, 1000, 4, 1) == 4 * 8 * 64 * 512      # matrices inside a block
+    assert nv(4096, 4096, 4, 1, 1024, 4, 1) == 0
+    assert mx(2048, 4096, 1, 0, 4096, 1, 0) == (16 + 32) * 32 * 512
+    assert nv(128, 4096, 1, 0, 4096, 1, 0) == 0 and nv(4096, 4096, 1, 0, 128, 1, 0) == 0
+    assert mx(1024, 2048, 1, 0, 2048, 1, 0) == 0                     # too small to pay
+    for f in (nv, mx):
+        for bad in [(-1, 64, 1, 0, 8, 1, 0), (4, 48, 1, 0, 8, 1, 0), (4, 64, 1, 2, 8, 1, 0),
+                    (4, 64, 2, 0, 8, 3, 0), (4, 64, 1, 0, 0, 1, 0)]:
+            assert f(*bad) == 0
+    big = (2048, 4096, 1, None, 0)
+    for ws, n, st in [(A, 48 * 64 * 512 - 1, 4), (P((1 << 20) + 128), 1 << 30, 3)]:
+        assert lib.trace_fp4_matmul_ws(A, A, A, *big, A, A, A, 4096, 1, 0, A, ws, n, None) == st
+    assert lib.trace_mx_matmul_ws(A, A, *big, A, A, 4096, 1, 0, A, A, 48 * 32 * 512 - 1, None) == 4
+    assert lib.trace_fp4_matmul_ws(A, A, A, 4, 48, 1, None, 0, A, A, A, 8, 1, 0, A, A, 0, None) == 2

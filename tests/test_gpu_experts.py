@@ -585,3 +585,55 @@ def test_combine_of_many_choices(k):
     s, m = terms.sum(1), np.abs(terms).sum(1)
     # one rounding to bf16 of a sum of k fused steps in fp32
     assert np.all(np.abs(out - s) <= 2.0 ** -8 * np.abs(s) + (1 + 2.0 ** -8) * k * 2.0 ** -24 * m)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tiled_a,tiled_w", [(False, False), (False, True), (True, False), (True, True)])
+@pytest.mark.parametrize("rows,n,cols,counts", [
+    (300, 1000, 352, None), (1111, 264, 96, None), (2048, 2050, 2080, None),
+    (900, 200, 608, [300, 0, 600]), (1500, 136, 1056, [129, 1000, None]),
+    (2500, 1000, 4128, [1100, 1400])])
+def test_product_of_pairs_on_copied_scales(fmt, tiled_a, tiled_w, rows, n, cols, counts):
+    """Scales in rows (of whole words or not), matrices that begin inside a
+    128-row block, k that ends inside a piece of four scale columns."""
+    _product_case(rows, n, cols, fmt, tiled_a, tiled_w, counts, seed=rows + cols)
+
+
+def test_product_with_a_workspace_of_the_caller():
+    """Poisoned before each call; the same bits as with one of its own, and
+    close to those without any copy."""
+    a = ops.capture(inputs.tiny_site(3, 700, 512).x_roll.to(DEV))
+    w = ops.capture(inputs.tiny_site(4, 384, 512).x_roll.to(DEV))
+    want = ops.fp4_matmul(a, w)
+    nbytes = ops.trace_matmul_workspace_bytes(False, 700, 512, 1, 0, 384, 1, 0)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+    for fill in (0x7F, 0xFF):
+        ws.fill_(fill)
+        assert torch.equal(ops.fp4_matmul(a, w, workspace=ws), want)
+    with pytest.raises(ops.TraceError):
+        ops.fp4_matmul(a, w, workspace=ws[:-256])
+    exact, mag = ref.product(_operand(a, 700, 512, "nvfp4"), _operand(w, 384, 512, "nvfp4"),
+                             a.gscale.cpu().numpy(), w.gscale.cpu().numpy(), [0, 700], 384)
+    out = torch.empty_like(want)
+    st = ops.library().trace_fp4_matmul(
+        a.codes.data_ptr(), a.scales.data_ptr(), a.gscale.data_ptr(), 700, 512, 1, None, 0,
+        w.codes.data_ptr(), w.scales.data_ptr(), w.gscale.data_ptr(), 384, 1, 0, out.data_ptr(),
+        torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    for o in (out, want):
+        assert np.all(np.abs(ref.f64(o) - exact) <= ref.product_bound(exact, mag, 512))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_products_of_rows_without_a_copy(fmt):
+    """The same through the entry points that take no workspace (single CTAs on
+    scales as they are)."""
+    f = ops.trace_matmul_workspace_bytes
+    try:
+        ops.trace_matmul_workspace_bytes = lambda *a: 0
+        for rows, n, cols, counts in [(300, 1000, 352, None), (1111, 264, 96, None),
+                                      (900, 200, 608, [300, 0, 600]), (700, 384, 512, None)]:
+            for ta, tw in ((False, False), (True, True), (False, True)):
+                _product_case(rows, n, cols, fmt, ta, tw, counts, seed=rows)
+    finally:
+        ops.trace_matmul_workspace_bytes = f
