@@ -33,7 +33,8 @@ constexpr int kMmThreads = 512;
 constexpr int kMmM = 128;            // w rows of a tile
 constexpr int kMmStageBytes = 128;   // code bytes per row and stage: 256 elements
 constexpr int kMmMaxStages = 8;
-constexpr uint32_t kMmTurnBytes = 12 * 16 * 40 * 2;  // output pieces being transposed
+constexpr uint32_t kMmTurnPiece = 16 * 32 * 2;          // an output piece: 16 tokens x 32 columns
+constexpr uint32_t kMmTurnBytes = 12 * kMmTurnPiece;  // one for each of up to 12 warps
 // CTAs that share a tile's k: clusters of 8 take 5 us longer to launch than
 // clusters of 4 (29 x 2048 x 4096: 12.9 us with 8, 7.6 with 4, 10.7 with 1).
 constexpr uint32_t kMmMaxSplit = 4;
@@ -75,7 +76,7 @@ struct OutScale {
   }
 };
 
-// 32 x 16 sums of a piece (tmem_ld_32x16) to bf16 pairs.
+// 16 sums of a lane to bf16 pairs.
 template <bool MX>
 __device__ __forceinline__ void scaled_bf16(const uint32_t* v, const OutScale& s, uint32_t* w) {
   if (MX || s.one) {
@@ -315,25 +316,17 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         : "memory");
 }
 
-// 32 lanes x 16 columns of an accumulator: lane / 4 (+ 8, 16, 24) are the rows
-// and 2 (lane % 4) (+ 8), and the next, the columns: v[0..1] row + 0, v[2..3]
-// row + 8, v[4..7] the same of the columns + 8, v[8..15] the rows + 16.
+// 32 lanes x 16 columns of an accumulator: a lane's row (output column) and 16
+// tokens.  (All of a tile in 120 cycles; in the shape that a transposing store
+// takes, 16 lanes x 256 bits, 420.)
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t addr, uint32_t* v) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-        : "=r"(v[8 * h]), "=r"(v[8 * h + 1]), "=r"(v[8 * h + 2]), "=r"(v[8 * h + 3]),
-          "=r"(v[8 * h + 4]), "=r"(v[8 * h + 5]), "=r"(v[8 * h + 6]), "=r"(v[8 * h + 7])
-        : "r"(addr + ((uint32_t)h << 20)));
-}
-// Four 8 x 8 tiles of 16-bit words, stored transposed; each lane gives the
-// address of one 16-byte row.
-__device__ __forceinline__ void st_matrix_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                            uint32_t d) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
-               "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(addr));
 }
 
 // Every load so far has arrived; no use of the words moves in front of the
@@ -561,7 +554,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t stage_at = (w_code + x_code + block_bytes * (1u + RB) + 1023u) & ~1023u;
   uint8_t* ring_p = smem_raw + (ring - smem_u32(smem_raw));
-  uint8_t* after = ring_p + sh.stages * stage_at;  // 12 warps x 16 tokens x 40 bf16, the table
+  uint8_t* after = ring_p + sh.stages * stage_at;  // pieces being turned, the table
   uint32_t* first_tile = reinterpret_cast<uint32_t*>(after + kMmTurnBytes);
   const uint32_t rank = cluster_rank();  // in a pair, or among the CTAs of a split
 
@@ -798,11 +791,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   } else if (warp >= 4 && warp < 4u + 4u * OUT) {
     // OUT warps per 32 lanes of tensor memory, each every OUT-th 16 tokens
     const uint32_t q = warp % 4u, odd = warp / 4u - 1u;
-    uint16_t* mine = reinterpret_cast<uint16_t*>(after) + (warp - 4u) * 16u * 40u;
-    // this lane's row of a transposed store: token and 8 columns of a 16 x 16 piece
-    const uint32_t st_at =
-        smem_u32(mine + ((lane / 16u) * 8u + lane % 8u) * 40u + (lane / 8u % 2u) * 8u);
-    const uint32_t tok = lane / 4u, col = (lane % 4u) * 8u;
+    // A piece of 16 tokens x 32 columns is turned as [token pair][column] words.
+    uint32_t* mine = reinterpret_cast<uint32_t*>(after + (warp - 4u) * kMmTurnPiece);
+    // Written out, a lane takes 8 columns of two tokens; the halves of its 32
+    // bytes in an order that has 8 lanes read different banks.
+    const uint32_t pair = lane / 4u, col = (lane % 4u) * 8u, flip = pair % 2u * 4u;
     Ring acc;
     bool ok = true;
     for (MmWalk t(t0, sh); ok && t.tt < token_tiles; t.next()) {
@@ -850,28 +843,36 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           float* part = reinterpret_cast<float*>(ring_p) + 32u * q;
 #pragma unroll
           for (uint32_t x = 0; x < 16u; ++x)
-            part[(c + x / 4u % 2u * 8u + lane % 4u * 2u + x % 2u) * 128u + x / 8u * 16u +
-                 x / 2u % 2u * 8u + lane / 4u] = __uint_as_float(v[i][x]);
+            part[(c + x) * 128u + lane] = __uint_as_float(v[i][x]);
           continue;
         }
         uint32_t w[8];
         scaled_bf16<MX>(v[i], scale, w);
         __syncwarp();
-        st_matrix_t(st_at, w[0], w[1], w[2], w[3]);
-        st_matrix_t(st_at + 32u, w[4], w[5], w[6], w[7]);
+#pragma unroll
+        for (uint32_t x = 0; x < 8u; ++x) mine[32u * x + lane] = w[x];
         __syncwarp();
         if (sh.out16) {
-#pragma unroll
-          for (uint32_t p = 0; p < 16u; p += 8u) {
-            const uint32_t row = c + tok + p;
-            if (row >= m.lead && row < m.tokens && (int64_t)j0 + col < sh.n)
-              *reinterpret_cast<uint4*>(to + (size_t)row * sh.n + col) =
-                  *reinterpret_cast<const uint4*>(mine + (tok + p) * 40u + col);
+          const uint4 a = *reinterpret_cast<const uint4*>(mine + 32u * pair + col + flip);
+          const uint4 b = *reinterpret_cast<const uint4*>(mine + 32u * pair + col + (4u - flip));
+          const uint4 lo = flip ? b : a, hi = flip ? a : b;  // columns + 0..3 and + 4..7
+          const uint32_t row = c + 2u * pair;
+          if ((int64_t)j0 + col < sh.n) {
+            uint16_t* at = to + (size_t)row * sh.n + col;
+            if (row >= m.lead && row < m.tokens)
+              *reinterpret_cast<uint4*>(at) =
+                  make_uint4(__byte_perm(lo.x, lo.y, 0x5410), __byte_perm(lo.z, lo.w, 0x5410),
+                             __byte_perm(hi.x, hi.y, 0x5410), __byte_perm(hi.z, hi.w, 0x5410));
+            if (row + 1u >= m.lead && row + 1u < m.tokens)
+              *reinterpret_cast<uint4*>(at + sh.n) =
+                  make_uint4(__byte_perm(lo.x, lo.y, 0x7632), __byte_perm(lo.z, lo.w, 0x7632),
+                             __byte_perm(hi.x, hi.y, 0x7632), __byte_perm(hi.z, hi.w, 0x7632));
           }
         } else if ((int64_t)j0 + lane < sh.n) {
           const uint32_t last = min(c + 16u, m.tokens);
           for (uint32_t row = max(c, m.lead); row < last; ++row)
-            to[(size_t)row * sh.n + lane] = mine[(row - c) * 40u + lane];
+            to[(size_t)row * sh.n + lane] =
+                (uint16_t)(mine[(row - c) / 2u * 32u + lane] >> ((row - c) % 2u * 16u));
         }
       }
     }
