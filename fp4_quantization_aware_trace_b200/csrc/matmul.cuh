@@ -22,6 +22,7 @@
 //              group starts anywhere), and zero what lies past the last k;
 //   warp 1      moves a stage's scales to tensor memory and issues its
 //              products;
+//   warp 3      finds the CTA's tiles ahead of the others and posts them;
 //   warps 4-11 read finished accumulators and write bf16 rows of out, while
 //              the next tile runs on the other accumulator.
 // Each role is one warp that runs alone on its scheduler, so a stage costs it
@@ -365,6 +366,7 @@ struct MmTile {
   uint32_t tokens;    // rows up to the group's last in this tile
   uint32_t j0;        // first output column
   bool product;       // false: a group without a matrix, its rows are zero
+  bool end;           // behind the last tile
 };
 
 __device__ __forceinline__ int64_t mm_bound(const int64_t* offs, int32_t g, const MmShape& sh) {
@@ -381,8 +383,8 @@ __device__ __forceinline__ int64_t mm_start(int64_t bound) {
   return CG == 2 ? bound & ~(int64_t)127 : bound;
 }
 
-// A role's walk over its tiles: token tile and w tile, t0 and every t_step-th
-// tile after it, without a division per tile.
+// A CTA's walk over its tiles: token tile and w tile, without a division per
+// tile.
 struct MmWalk {
   uint32_t tt, jt, dt, dj, n_tiles;
   __device__ __forceinline__ MmWalk(uint32_t t0, const MmShape& sh)
@@ -424,7 +426,30 @@ __device__ __forceinline__ MmTile mm_tile(const MmWalk& at, const uint32_t* firs
   m.tokens = (uint32_t)((end < from + sh.nt ? end : from + sh.nt) - m.row0);
   m.j0 = at.jt * (CG * kMmM);
   m.product = m.group < sh.matrices;
+  m.end = false;
   return m;
+}
+
+// One warp finds the CTA's tiles ahead of the others (a tile's group, its bounds
+// and global scales are some 1000 cycles of dependent loads) and posts them.
+constexpr uint32_t kMmPosts = 3;
+struct MmPosts {
+  MmTile tile[kMmPosts];
+  OutScale scale[kMmPosts];
+  u64 posted[kMmPosts], taken[kMmPosts];
+};
+
+// The next posted tile, for a warp; false behind the last one (or when the CTA
+// has given up).
+__device__ __forceinline__ bool mm_next(Ring* at, MmPosts* posts, MmTile* m, OutScale* scale,
+                                        volatile uint32_t* gave_up) {
+  if (!mm_wait(smem_u32(&posts->posted[at->at]), at->parity, gave_up)) return false;
+  *m = posts->tile[at->at];
+  if (scale != nullptr) *scale = posts->scale[at->at];
+  __syncwarp();
+  if (threadIdx.x % 32u == 0u) mbar_arrive(smem_u32(&posts->taken[at->at]));
+  at->next(kMmPosts);
+  return !m->end;
 }
 
 // first_tile[0 .. groups] by a scan over the CTA.
@@ -547,6 +572,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   constexpr uint32_t PIECES = ((PAIR ? kMmPairTokens : RB == 2 ? kMmTokens : 128u) / 16u + OUT - 1u) / OUT;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) u64 full[kMmMaxStages], empty[kMmMaxStages], acc_full[2], acc_empty[2];
+  __shared__ __align__(8) MmPosts posts;
   __shared__ uint32_t tmem_base_s, warp_sum[kMmThreads / 32];
   __shared__ volatile uint32_t gave_up;
   const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32u, 0), lane = threadIdx.x % 32u;
@@ -567,6 +593,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     for (uint32_t a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&acc_full[a]), 1);
       mbar_init(smem_u32(&acc_empty[a]), 4 * OUT * CG);
+    }
+    for (uint32_t a = 0; a < kMmPosts; ++a) {
+      mbar_init(smem_u32(&posts.posted[a]), 1);
+      // the warps that copy, that issue and that write out
+      mbar_init(smem_u32(&posts.taken[a]), 1 + (PAIR ? (rank == 0 ? 1 : 0) : 1 + 4) + 4 * OUT);
     }
     gave_up = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -605,9 +636,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   const uint32_t acc_cols = (sh.nt + 31u) & ~31u;
   constexpr uint32_t sf_cols = 4u * ATOMS * (1u + RB);  // tensor-memory columns of a stage's scales
   const uint32_t sf_base = tmem + sh.accs * acc_cols;
-  // this CTA's tiles, and its part of k
+  // this CTA's part of k
   const uint32_t team = PAIR ? 2u : sh.split;
-  const uint32_t t0 = blockIdx.x / team;
   const uint32_t k_rank = PAIR ? 0u : rank;
   const uint32_t k0 = k_rank * sh.ksteps / sh.split, k1 = (k_rank + 1u) * sh.ksteps / sh.split;
   const uint32_t j_rank = PAIR ? rank * kMmM : 0u;
@@ -617,8 +647,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     r.parity = 1u;  // the first round finds every slot empty
     bool ok = true;
     const uint32_t c4s = (sh.scols + 3u) / 4u, bulk_steps = sh.scols / (4u * ATOMS);
-    for (MmWalk t(t0, sh); ok && t.tt < token_tiles; t.next()) {
-      const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
+    MmTile m;
+    Ring next;
+    while (ok && mm_next(&next, &posts, &m, nullptr, &gave_up)) {
       if (!m.product) continue;
       const int64_t wr = m.group * sh.n + m.j0 + j_rank;
       const int32_t w_row = (int32_t)uniform((uint32_t)wr);
@@ -673,15 +704,16 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
       }
     }
-    if (!ok)  // let the copies in flight land before the CTA leaves
+    if (gave_up)  // let the copies in flight land before the CTA leaves
       for (int z = 0; z < 1000; ++z) __nanosleep(1000);
   } else if (warp >= 12 && !PAIR) {
     const uint32_t quarter = warp - 12u;
     Ring r;
     r.parity = 1u;
     bool ok = true;
-    for (MmWalk t(t0, sh); ok && t.tt < token_tiles; t.next()) {
-      const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
+    MmTile m;
+    Ring next;
+    while (ok && mm_next(&next, &posts, &m, nullptr, &gave_up)) {
       if (!m.product) continue;
       const int64_t wr = m.group * sh.n + m.j0 + j_rank;
       const ScaleSrc sw = scale_src(ws, sh.w_tiled, sh.w_bytes, wr, sh.n * sh.matrices, sh.scols,
@@ -724,8 +756,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     uint32_t bar = smem_u32(&full[0]), parity = 0u;
     bool ok = true, ready = false, any = false;
     uint32_t at = ring, freed = 0u, freed_parity = 0u;
-    for (MmWalk t(t0, sh); ok && t.tt < token_tiles; t.next()) {
-      const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
+    MmTile m;
+    Ring next;
+    while (ok && mm_next(&next, &posts, &m, nullptr, &gave_up)) {
       if (!m.product) continue;
       const uint32_t width = uniform(mm_width<CG>(m.tokens));
       const uint32_t d = uniform(tmem + acc.at * acc_cols), idesc = mm_idesc<MX, CG>(width);
@@ -788,6 +821,27 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     }
     // the products in flight must end before tensor memory is freed
     if (any) mm_wait(freed, freed_parity, &gave_up);
+  } else if (warp == 3) {
+    Ring at;
+    at.parity = 1u;
+    for (MmWalk t(blockIdx.x / team, sh);; t.next()) {
+      MmTile m;
+      m.end = t.tt >= token_tiles;
+      OutScale scale{1.0f, 1.0f, 1.0f, true};
+      if (!m.end) {
+        m = mm_tile<CG>(t, first_tile, offs, sh);
+        if (!MX && m.product) scale = make_out_scale(ag[m.group], wg[m.group]);
+      }
+      if (!mm_wait(smem_u32(&posts.taken[at.at]), at.parity, &gave_up)) break;
+      if (lane == 0) {
+        posts.tile[at.at] = m;
+        posts.scale[at.at] = scale;
+        mbar_arrive(smem_u32(&posts.posted[at.at]));
+      }
+      __syncwarp();
+      at.next(kMmPosts);
+      if (m.end) break;
+    }
   } else if (warp >= 4 && warp < 4u + 4u * OUT) {
     // OUT warps per 32 lanes of tensor memory, each every OUT-th 16 tokens
     const uint32_t q = warp % 4u, odd = warp / 4u - 1u;
@@ -798,11 +852,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const uint32_t pair = lane / 4u, col = (lane % 4u) * 8u, flip = pair % 2u * 4u;
     Ring acc;
     bool ok = true;
-    for (MmWalk t(t0, sh); ok && t.tt < token_tiles; t.next()) {
-      const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
-      OutScale scale{1.0f, 1.0f, 1.0f, true};
+    MmTile m;
+    OutScale scale;
+    Ring next;
+    while (ok && mm_next(&next, &posts, &m, &scale, &gave_up)) {
       if (m.product) {
-        if (!MX) scale = make_out_scale(ag[m.group], wg[m.group]);
         if (!(ok = mm_wait(smem_u32(&acc_full[acc.at]), acc.parity, &gave_up))) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       }
@@ -881,11 +935,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     // Every CTA of the cluster holds a part of the sums of one tile; each adds
     // up every split-th token, the parts in the order of k.
     cluster_sync();
-    const MmWalk t(t0, sh);
-    if (t.tt < token_tiles) {
-      const MmTile m = mm_tile<CG>(t, first_tile, offs, sh);
-      const OutScale scale =
-          MX ? OutScale{1.0f, 1.0f, 1.0f, true} : make_out_scale(ag[m.group], wg[m.group]);
+    if (!gave_up) {
+      const MmTile m = posts.tile[0];
+      const OutScale scale = posts.scale[0];
       const uint32_t j = threadIdx.x % 128u;
       for (uint32_t tk = rank + threadIdx.x / 128u * sh.split; tk < m.tokens;
            tk += kMmThreads / 128u * sh.split) {
