@@ -40,6 +40,7 @@ constexpr uint32_t kMmTurnBytes = 12 * kMmTurnPiece;  // one for each of up to 1
 // clusters of 4 (29 x 2048 x 4096: 12.9 us with 8, 7.6 with 4, 10.7 with 1).
 constexpr uint32_t kMmMaxSplit = 4;
 constexpr uint32_t kMmTokens = 192, kMmPairTokens = 256;  // of the largest tiles
+constexpr uint32_t kMmPairBox = kMmPairTokens / 4;        // token rows a CTA of a pair copies at a time
 constexpr uint32_t kMmTmemCols = 512;
 // Polls of one wait before a CTA gives up (each try_wait itself suspends):
 // a guard, every wait ends as its copies and products do.
@@ -660,7 +661,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         const int32_t wb = (int32_t)uniform((uint32_t)m.group * sh.w_blocks + (m.j0 + j_rank) / 128u);
         const int32_t row = (int32_t)uniform((uint32_t)m.row0), xb = row / 128;
         const int32_t xr = row + (int32_t)uniform(rank * (width / 2u));
-        const uint32_t bytes = 2u * (w_code + x_code + (two ? 3u : 2u) * block_bytes);
+        // token codes in boxes of 64 rows, as many as the tile has
+        const bool more = width / 2u > kMmPairBox;
+        const uint32_t bytes = 2u * (w_code + (more ? 2u : 1u) * kMmPairBox * kMmStageBytes +
+                                     (two ? 3u : 2u) * block_bytes);
         for (uint32_t k = 0; k < sh.ksteps; ++k, r.next(sh.stages)) {
           const uint32_t at = uniform(ring + r.at * stage_at), sc = at + w_code + x_code;
           const uint32_t own = smem_u32(&full[r.at]), bar = peer_smem(own, 0);
@@ -669,6 +673,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           if (rank == 0) mbar_expect(own, bytes);
           tma_load_2d<CG>(at, &maps.w, (int32_t)(k * kMmStageBytes), w_row, bar);
           tma_load_2d<CG>(at + w_code, &maps.a, (int32_t)(k * kMmStageBytes), xr, bar);
+          if (more)
+            tma_load_2d<CG>(at + w_code + kMmPairBox * kMmStageBytes, &maps.a,
+                            (int32_t)(k * kMmStageBytes), xr + (int32_t)kMmPairBox, bar);
           tma_load_2d<CG>(sc, &maps.ws, (int32_t)(k * ATOMS * 64u), wb, bar);
           tma_load_2d<CG>(sc + block_bytes, &maps.as, (int32_t)(k * ATOMS * 64u), xb, bar);
           if (two)

@@ -462,7 +462,8 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
       sh.split *= 2;
   sh.out16 = n % 8 == 0;
   MmMaps maps;
-  int st = code_map(&maps.a, a_codes, (uint64_t)rows, (uint64_t)cols / 2, sh.nt / cg);
+  int st = code_map(&maps.a, a_codes, (uint64_t)rows, (uint64_t)cols / 2,
+                    pair ? kMmPairBox : sh.nt);
   if (!st) st = code_map(&maps.w, w_codes, (uint64_t)n * matrices, (uint64_t)cols / 2, kMmM);
   if (!st && pair) st = scale_map(&maps.as, a_scales, (uint64_t)rows, sh.scols, kAtoms);
   if (!st && pair) st = scale_map(&maps.ws, w_scales, (uint64_t)sh.w_blocks * matrices * 128u, sh.scols, kAtoms);
