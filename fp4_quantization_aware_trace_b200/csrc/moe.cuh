@@ -212,41 +212,58 @@ __global__ void __launch_bounds__(kThreads)
 
 // Back to token order: out[t] = sum_j weights[t, j] y[rows[t, j]] in fp32, in
 // the order of j, rounded once; weights == NULL sums with weight one (the
-// gradient of dispatch).
-__global__ void __launch_bounds__(kThreads, 2)
+// gradient of dispatch).  Bound by reads of rows in no order: 302 MB (8192 x 8
+// rows of 2048) in 59 us.  Two CTAs per SM, each warp with eight rows of 1 KB
+// on their way, and a walk over the units that reads the next row numbers
+// early; a CTA for every eight units (32 per SM) takes 67 us, half as many
+// columns per warp with twice the warps 61 us.
+constexpr int kCombinePerSm = 2;
+__global__ void __launch_bounds__(kThreads, kCombinePerSm)
     k_moe_combine(const V8* __restrict__ y, MoeShape sh, const int32_t* __restrict__ rows,
                   const float* __restrict__ weights, V8* __restrict__ out) {
   constexpr uint32_t kBatch = 8u;  // rows on their way at a time
   pdl_begin();
   const uint32_t lane = threadIdx.x % 32u;
-  const u64 units = (u64)sh.tokens * sh.segs;
-  for (u64 u = (u64)blockIdx.x * (kThreads / 32) + threadIdx.x / 32u; u < units;
-       u += (u64)gridDim.x * (kThreads / 32)) {
+  const u64 units = (u64)sh.tokens * sh.segs, stride = (u64)gridDim.x * (kThreads / 32);
+  u64 u = (u64)blockIdx.x * (kThreads / 32) + threadIdx.x / 32u;
+  // Lane j holds the row number and weight of choice j of a batch for all; a
+  // unit's first ones are read while the unit before it waits for its rows.
+  int32_t row = -1;
+  float f = 0.0f;
+  auto choices = [&](uint32_t t, uint32_t j0) {
+    const uint32_t s = t * sh.k + j0 + lane;
+    const bool has = lane < kBatch && j0 + lane < sh.k;
+    row = has ? rows[s] : -1;
+    f = weights == nullptr ? 1.0f : has ? weights[s] : 0.0f;
+  };
+  if (u < units) choices((uint32_t)(u / sh.segs), 0u);
+  for (; u < units; u += stride) {
     const uint32_t t = (uint32_t)(u / sh.segs), w = (uint32_t)(u % sh.segs) * 32u + lane;
     const bool in = w < sh.lanes;
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
     for (uint32_t j0 = 0; j0 < sh.k; j0 += kBatch) {
-      // lane j reads the row number and weight of choice j0 + j for all
-      const uint32_t left = min(kBatch, sh.k - j0), s = t * sh.k + j0 + lane;
-      const int32_t my_row = lane < left ? rows[s] : -1;
-      const float my_f = weights == nullptr ? 1.0f : lane < left ? weights[s] : 0.0f;
+      if (j0 > 0u) choices(t, j0);
+      const int32_t my_row = row;
+      const float my_f = f;
       V8 v[kBatch];
 #pragma unroll
       for (uint32_t q = 0; q < kBatch; ++q) {
         const uint32_t r = (uint32_t)__shfl_sync(0xFFFFFFFFu, my_row, q);
         if (in && r < sh.slots) v[q] = ld_block_stream(y + (size_t)r * sh.lanes + w);
       }
+      if (j0 + kBatch >= sh.k && u + stride < units)
+        choices((uint32_t)((u + stride) / sh.segs), 0u);
 #pragma unroll
       for (uint32_t q = 0; q < kBatch; ++q) {
         const uint32_t r = (uint32_t)__shfl_sync(0xFFFFFFFFu, my_row, q);
-        const float f = __shfl_sync(0xFFFFFFFFu, my_f, q);
+        const float wq = __shfl_sync(0xFFFFFFFFu, my_f, q);
         if (!(in && r < sh.slots)) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          acc[2 * i] = __fmaf_rn(f, bf16_lo(v[q].w[i]), acc[2 * i]);
-          acc[2 * i + 1] = __fmaf_rn(f, bf16_hi(v[q].w[i]), acc[2 * i + 1]);
+          acc[2 * i] = __fmaf_rn(wq, bf16_lo(v[q].w[i]), acc[2 * i]);
+          acc[2 * i + 1] = __fmaf_rn(wq, bf16_hi(v[q].w[i]), acc[2 * i + 1]);
         }
       }
     }

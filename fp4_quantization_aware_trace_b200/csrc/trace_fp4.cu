@@ -339,7 +339,7 @@ int code_map(CUtensorMap* map, const uint8_t* codes, uint64_t rows, uint64_t byt
   const cuuint32_t box[2] = {(cuuint32_t)kMmStageBytes, box_rows}, step[2] = {1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)codes, dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? TRACE_OK
              : TRACE_ERR_CUDA;
@@ -1122,11 +1122,11 @@ static int moe_shape(int64_t tokens, int64_t k, int64_t cols, MoeShape* sh) {
   return TRACE_OK;
 }
 
-static int moe_grid(u64 units, int* grid) {
+static int moe_grid(u64 units, int* grid, int per_sm = kGridPerSm) {
   const int sms = sm_count();
   if (sms <= 0) return TRACE_ERR_CUDA;
   const u64 ctas = (units + kThreads / 32 - 1) / (kThreads / 32);
-  const u64 most = (u64)sms * kGridPerSm;
+  const u64 most = (u64)sms * per_sm;
   *grid = (int)(ctas < most ? ctas : most);
   return TRACE_OK;
 }
@@ -1153,7 +1153,7 @@ int trace_moe_combine(const uint16_t* y, int64_t tokens, int64_t k, int64_t cols
   if (!y || !rows || !out) return TRACE_ERR_NULL;
   if (!aligned(y, 32) || !aligned(rows, 4) || !aligned(weights, 4) || !aligned(out, 32))
     return TRACE_ERR_ALIGN;
-  if ((st = moe_grid((u64)sh.tokens * sh.segs, &grid))) return st;
+  if ((st = moe_grid((u64)sh.tokens * sh.segs, &grid, kCombinePerSm))) return st;
   return launch(k_moe_combine, grid, (cudaStream_t)stream, (const V8*)y, sh, rows, weights,
                 (V8*)out);
 }
