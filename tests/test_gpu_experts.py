@@ -637,3 +637,122 @@ def test_products_of_rows_without_a_copy(fmt):
                 _product_case(rows, n, cols, fmt, ta, tw, counts, seed=rows)
     finally:
         ops.trace_matmul_workspace_bytes = f
+
+
+# ---------------------------------------------------------------------------
+# Sizes past 32 bits, nothing at all, and graphs of both directions
+# ---------------------------------------------------------------------------
+
+def test_product_with_more_than_2_31_outputs():
+    rows, n, cols = 540000, 4096, 64
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    x = torch.randn(rows, cols, generator=g, device=DEV).bfloat16()
+    w = ops.capture_tiled(inputs.tiny_site(2, n, cols).x_roll.to(DEV))
+    for cap in (ops.capture_tiled(x), ops.capture(x)):
+        out = ops.fp4_matmul(cap, w, cols)
+        codes, scols = cap.codes.view(rows, cols // 2), cols // 16
+        s = cap.scales
+        if s.dim() != 2:  # a 128-row block is 512 bytes here: 4 scale columns
+            s = s.view(-1, 32, 4, 4).permute(0, 2, 1, 3).reshape(-1, scols)[:rows]
+        wv = _operand(w, n, cols, "nvfp4")
+        for lo in (0, 262143, 524287, rows - 130):  # the last three past 2^30 and 2^31 elements
+            part = ref.operand(codes[lo:lo + 130].cpu().numpy(), s[lo:lo + 130].cpu().numpy(), 130,
+                               cols, "nvfp4")
+            exact, mag = ref.product(part, wv, cap.gscale.cpu().numpy(), w.gscale.cpu().numpy(),
+                                     [0, 130], n)
+            assert np.all(np.abs(ref.f64(out[lo:lo + 130]) - exact)
+                          <= ref.product_bound(exact, mag, cols))
+        del out
+
+
+def test_tokens_with_more_than_2_31_elements():
+    tokens, k, cols, experts = 300000, 8, 1024, 16
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    ids = torch.randint(0, experts, (tokens, k), generator=g, device=DEV)
+    route = ops.moe_sort(ids, experts)
+    x = torch.randn(tokens, cols, generator=g, device=DEV).bfloat16()
+    y = ops.moe_dispatch(x, route)
+    at = torch.tensor([0, 5, 2 ** 31 // cols - 1, 2 ** 31 // cols, tokens * k - 1], device=DEV)
+    assert torch.equal(y[at], x[(route.slots[at] // k).long()])
+    # 1/8 of a token's own value eight times: exact in every step
+    weights = torch.full((tokens, k), 0.125, device=DEV)
+    assert torch.equal(ops.moe_combine(y, route, weights), x)
+    dy, dw = ops.moe_combine_bwd(x, y, route, weights)
+    rows = route.rows.long()
+    for t in (0, 131071, 262145, tokens - 1):
+        assert torch.equal(dy[rows[t]], (x[t] * 0.125).expand(k, cols))
+        want = (x[t].double() ** 2).sum()
+        assert bool(((dw[t].double() - want).abs() <= (cols / 32 + 5) * 2.0 ** -24 * want).all())
+
+
+def test_no_tokens():
+    ids = torch.empty(0, 4, dtype=torch.int64, device=DEV)
+    route = ops.moe_sort(ids, 6)
+    assert route.offsets.tolist() == [0] * 8 and route.rows.shape == (0, 4)
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    y = ops.moe_dispatch(x, route)
+    w = torch.empty(0, 4, device=DEV, requires_grad=True)
+    out = ops.moe_combine(y, route, w)
+    dx, dw = torch.autograd.grad(out, (x, w), torch.empty_like(out))
+    assert y.shape == out.shape == dx.shape == (0, 64) and dw.shape == (0, 4)
+
+
+def test_dropped_rows_are_never_read():
+    """NaN and infinities in the last group's rows, in their gradient and in
+    the weights of dropped slots reach nothing."""
+    tokens, k, experts, cols = 40, 3, 5, 96
+    route, (offsets, rows, _) = _route(tokens, k, experts, 2, dropped=0.4)
+    live, lo = torch.from_numpy(rows >= 0).to(DEV), int(offsets[experts])
+    y = torch.randn(tokens * k, cols, generator=_gen(1)).bfloat16().to(DEV)
+    w = torch.randn(tokens, k, generator=_gen(2)).to(DEV)
+    do = torch.randn(tokens, cols, generator=_gen(3)).bfloat16().to(DEV)
+    yb, wb = y.clone(), w.clone()
+    yb[lo:] = float("nan")
+    yb[lo::2] = float("inf")
+    wb[~live] = float("nan")
+    for a, b in zip((ops.moe_combine(y, route, w), *ops.moe_combine_bwd(do, y, route, w),
+                     ops.moe_dispatch_bwd(y, route)),
+                    (ops.moe_combine(yb, route, wb), *ops.moe_combine_bwd(do, yb, route, wb),
+                     ops.moe_dispatch_bwd(yb, route))):
+        assert torch.equal(a, b) and bool(torch.isfinite(b).all())
+
+
+def test_both_directions_in_a_graph():
+    """Forward and backward captured together and replayed on other inputs.
+    No eager autograd graph of the leaves is alive during capture: PyTorch
+    cannot capture a backward pass beside one."""
+    tokens, k, experts, cols = 50, 4, 9, 512
+    route, _ = _route(tokens, k, experts, 4)
+    x = torch.randn(tokens, cols, generator=_gen(1)).bfloat16().to(DEV).requires_grad_()
+    w = torch.rand(tokens, k, generator=_gen(2)).to(DEV).requires_grad_()
+    do = torch.randn(tokens, cols, generator=_gen(3)).bfloat16().to(DEV)
+
+    def both():
+        out = ops.moe_combine(ops.moe_dispatch(x, route), route, w)
+        return (out.detach(), *torch.autograd.grad(out, (x, w), do))
+
+    eager = both()
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=s):
+        held = both()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(eager, held))
+    with torch.no_grad():
+        x.copy_(torch.randn(tokens, cols, generator=_gen(5)).bfloat16())
+        w.copy_(torch.rand(tokens, k, generator=_gen(6)))
+    graph.replay()
+    again = both()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(again, held))
+
+
+def test_no_second_derivative():
+    route, _ = _route(5, 2, 3, 1)
+    x = torch.randn(5, 64).bfloat16().to(DEV).requires_grad_()
+    (dx,) = torch.autograd.grad(ops.moe_dispatch(x, route).float().pow(2).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.float().sum().backward()
