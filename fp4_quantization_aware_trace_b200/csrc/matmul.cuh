@@ -15,26 +15,44 @@
 //
 // One persistent CTA per SM walks tiles; its warps are specialised:
 //   warp 0      copies both operands' codes by TMA, 256 k-elements (128 bytes
-//              per row, 128-byte swizzle) per stage of a shared-memory ring,
-//              and tiled scales whose 128-row block is the tile's own;
-//   warps 12-15 copy all other scales into the ring in the 128 x 4 tiled order
-//              the tensor core wants, from either layout and at any row (a
-//              group starts anywhere), and zero what lies past the last k;
-//   warp 1      moves a stage's scales to tensor memory and issues its
-//              products;
+//               per row, 128-byte swizzle) per stage of a shared-memory ring,
+//               and tiled scales whose 128-row block is the tile's own;
+//   warp 1      moves a stage's scales to tensor memory and issues its products;
 //   warp 3      finds the CTA's tiles ahead of the others and posts them;
-//   warps 4-11 read finished accumulators and write bf16 rows of out, while
-//              the next tile runs on the other accumulator.
-// Each role is one warp that runs alone on its scheduler, so a stage costs it
-// its instructions' latencies: ring positions are counters and not quotients,
-// and the loops over a stage's parts are unrolled.
+//   warps 4-11  read finished accumulators and write bf16 rows of out;
+//   warps 12-15 copy all other scales into the ring in the 128 x 4 tiled order
+//               the tensor core wants, from either layout and at any row (a
+//               group starts anywhere), and zero what lies past the last k.
+// Large products are done by pairs of CTAs (M = 256, N up to 256): each CTA
+// copies its own rows of w and half of the tokens, so a stage moves 39 KB into
+// an SM for 512 cycles of products and not 47 KB for 384.  Their scales all
+// come by TMA, and warps 12-15 write out with the others.
+//
+// Tensor memory (512 columns) holds one accumulator of 256 or 192 tokens and 5
+// or more stages of scales, or two accumulators of up to 128: of a large one the
+// next tile's products wait until it has been read out (120 cycles of reads in a
+// bubble of 1500), which costs less than two of 192 with only two stages of
+// NVFP4 scales beside them (16384 x 4096 x 2048: 92 us).  The issuing warp's own
+// instructions are what a stage costs besides: 12 copies of scales and 4
+// products issue in 250 cycles if nothing is waited for in between.
+//
+// Measured, back to back in a graph (us; of 4 times the measured bf16 rate or
+// of the measured copy bandwidth):
+//   16384 x 4096 x 2048 NVFP4               67   4.1 PFLOP/s, 0.62
+//   4099 x 4096 x 4096 MXFP4                28.5 4.8 PFLOP/s, 0.73
+//   65536 x 1536 x 2048, 128 experts NVFP4  132  3.1 PFLOP/s, 0.58
+//   512 x 1536 x 2048, 128 experts NVFP4    41   5.6 TB/s, 0.85
+//   1 x 4096 x 4096 NVFP4                   7.0  one wave: launch and latency
+// What bounds the large ones: the tensor core is busy 0.53 of the time (0.69
+// without any output); writing out (2 bytes per token and column) takes 20 of
+// the 67 us in bubbles and in traffic beside the copies of operands.
 #pragma once
 
 constexpr int kMmThreads = 512;
 constexpr int kMmM = 128;            // w rows of a tile
 constexpr int kMmStageBytes = 128;   // code bytes per row and stage: 256 elements
 constexpr int kMmMaxStages = 8;
-constexpr uint32_t kMmTurnPiece = 16 * 32 * 2;          // an output piece: 16 tokens x 32 columns
+constexpr uint32_t kMmTurnPiece = 16 * 32 * 2;        // an output piece: 16 tokens x 32 columns
 constexpr uint32_t kMmTurnBytes = 12 * kMmTurnPiece;  // one for each of up to 12 warps
 // CTAs that share a tile's k: clusters of 8 take 5 us longer to launch than
 // clusters of 4 (29 x 2048 x 4096: 12.9 us with 8, 7.6 with 4, 10.7 with 1).
@@ -158,9 +176,8 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0u;
 }
 
-// A value that every lane of a warp holds: from here on in uniform registers,
-// which what the tensor core and the copy engine are given has to be in (a
-// stage's 12 scale copies and 4 products issue in 250 cycles instead of 350).
+// A value that every lane of a warp holds, said to be so: what the tensor core
+// and the copy engine are given has to be in uniform registers.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // Up to 256 polls for a phase to end.
@@ -370,6 +387,7 @@ struct MmTile {
   bool end;           // behind the last tile
 };
 
+// Offsets are clamped to the rows there are, whatever they hold.
 __device__ __forceinline__ int64_t mm_bound(const int64_t* offs, int32_t g, const MmShape& sh) {
   if (offs == nullptr) return g == 0 ? 0 : sh.rows;
   const int64_t v = offs[g];
@@ -423,10 +441,11 @@ __device__ __forceinline__ MmTile mm_tile(const MmWalk& at, const uint32_t* firs
   const int64_t from = mm_start<CG>(begin) + (int64_t)(tt - first) * sh.nt;
   m.row0 = CG == 2 && begin - from >= 64 ? from + 64 : from;
   m.lead = begin > m.row0 ? (uint32_t)(begin - m.row0) : 0u;
-  const int64_t end = mm_bound(offs, m.group + 1, sh);
-  m.tokens = (uint32_t)((end < from + sh.nt ? end : from + sh.nt) - m.row0);
+  const int64_t end = mm_bound(offs, m.group + 1, sh), to = end < from + sh.nt ? end : from + sh.nt;
+  // (no tile of a valid table is empty; one of offsets that go down could be)
+  m.tokens = from >= 0 && to > m.row0 ? (uint32_t)(to - m.row0) : 0u;
   m.j0 = at.jt * (CG * kMmM);
-  m.product = m.group < sh.matrices;
+  m.product = m.group < sh.matrices && m.tokens > 0u;
   m.end = false;
   return m;
 }

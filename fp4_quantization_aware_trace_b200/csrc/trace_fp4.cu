@@ -3,15 +3,17 @@
 // fake-quant forward, the masked straight-through backward and the
 // round-to-nearest comparator; with them the full-information guided
 // forward, the MXFP4 (W4A4) and W4A8 variants, the 128 x 4 tiled scale
-// layout, capture's two passes for sharded or streamed tensors, and the
-// mismatch-distance histogram.
+// layout, capture's two passes for sharded or streamed tensors, the
+// mismatch-distance histogram, and the FP4 experts' operators: the routing
+// sort, tokens into expert order and back, the product of captured operands.
 //
 // Method: rcap.io post "TRACE: Rollout-Guided Quantization-Aware Training for
 // FP4" (2026-10-06), sections "rollout-guided rounding" and "compact cache"
 // and its pseudocode listing (capture; QAT forward).  The number format and
 // the layouts are documented in include/trace_fp4.h.
 //
-// Design (everything here is HBM-bound elementwise work; no tensor cores):
+// Design (HBM-bound elementwise work without tensor cores, but for the product,
+// which matmul.cuh describes):
 //   * One thread owns one 16-element scale block: a single 32-byte load
 //     (ld.global.v8) brings it in, so a warp reads 1 KiB contiguous per
 //     instruction and the per-block work (scale decode, reciprocal) is done
@@ -58,7 +60,7 @@
 // File layout: this file holds the host side and the C ABI; the kernels are
 // in csrc/*.cuh, included below inside this file's anonymous namespace (one
 // translation unit): common.cuh (shared device helpers), nvfp4.cuh, mx.cuh,
-// mismatch.cuh, util.cuh.
+// mismatch.cuh, util.cuh, moe.cuh (sort, dispatch, combine), matmul.cuh.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
