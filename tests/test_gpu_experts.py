@@ -756,3 +756,12 @@ def test_no_second_derivative():
     (dx,) = torch.autograd.grad(ops.moe_dispatch(x, route).float().pow(2).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError):
         dx.float().sum().backward()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,n,cols", [(4100, 1030, 192), (9000, 300, 576), (3329, 776, 1088)])
+def test_product_of_pairs_in_several_waves(fmt, rows, n, cols):
+    """More tiles of 128 tokens than run at once: tiles of 256, some CTAs with
+    more of them than others."""
+    assert -(-rows // 128) * -(-n // 256) > torch.cuda.get_device_properties(0).multi_processor_count // 2
+    _product_case(rows, n, cols, fmt, True, True, seed=rows + n)
