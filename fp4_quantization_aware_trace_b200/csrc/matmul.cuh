@@ -36,16 +36,18 @@
 // instructions are what a stage costs besides: 12 copies of scales and 4
 // products issue in 250 cycles if nothing is waited for in between.
 //
-// Measured, back to back in a graph (us; of 4 times the measured bf16 rate or
-// of the measured copy bandwidth):
-//   16384 x 4096 x 2048 NVFP4               67   4.1 PFLOP/s, 0.62
-//   4099 x 4096 x 4096 MXFP4                28.5 4.8 PFLOP/s, 0.73
-//   65536 x 1536 x 2048, 128 experts NVFP4  132  3.1 PFLOP/s, 0.58
-//   512 x 1536 x 2048, 128 experts NVFP4    41   5.6 TB/s, 0.85
-//   1 x 4096 x 4096 NVFP4                   7.0  one wave: launch and latency
-// What bounds the large ones: the tensor core is busy 0.53 of the time (0.69
-// without any output); writing out (2 bytes per token and column) takes 20 of
-// the 67 us in bubbles and in traffic beside the copies of operands.
+// Measured, back to back in a graph (of 4 times the measured bf16 rate, or of
+// the measured copy bandwidth):
+//   16384 x 4096 x 2048 NVFP4                65 us   4.2 PFLOP/s, 0.64
+//   4099 x 4096 x 4096 MXFP4                 28.2 us 4.9 PFLOP/s, 0.74
+//   65536 x 1536 x 2048, 128 experts NVFP4   130 us  3.2 PFLOP/s, 0.59
+//   512 x 1536 x 2048, 128 experts NVFP4     41 us   5.6 TB/s, 0.85
+//   1 x 4096 x 4096 NVFP4                    7.0 us  one wave: launch and latency
+// What bounds the large ones: the tensor core is busy a little over half of the
+// time; reading an accumulator out, and the traffic of the output beside that of
+// the operands, take the rest (without any output 16384 x 4096 x 2048 takes 45
+// us).  With calls back to back for a second the 1 kW limit lowers the clock to
+// 1.6 GHz and the first takes 78 us.
 #pragma once
 
 constexpr int kMmThreads = 512;
@@ -54,6 +56,7 @@ constexpr int kMmStageBytes = 128;   // code bytes per row and stage: 256 elemen
 constexpr int kMmMaxStages = 8;
 constexpr uint32_t kMmTurnPiece = 16 * 32 * 2;        // an output piece: 16 tokens x 32 columns
 constexpr uint32_t kMmTurnBytes = 12 * kMmTurnPiece;  // one for each of up to 12 warps
+constexpr uint32_t kMmBox = 32 * 32 * 2;             // 32 rows x 32 columns of out, for each of 12 warps
 // CTAs that share a tile's k: clusters of 8 take 5 us longer to launch than
 // clusters of 4 (29 x 2048 x 4096: 12.9 us with 8, 7.6 with 4, 10.7 with 1).
 constexpr uint32_t kMmMaxSplit = 4;
@@ -73,7 +76,7 @@ struct MmShape {
   uint32_t w_blocks;           // ceil(n / 128): of pairs, a matrix's 128-row blocks of scales
   uint32_t ksteps;             // stages of a whole product
   uint32_t stages, accs, sf_slots;
-  uint32_t step_tokens, step_j;  // token and w tiles from one of a CTA's (a team's) to its next
+  uint32_t n_lo, step_hi, step_lo;  // see MmWalk; from one of a CTA's (a team's) tiles to its next
   uint32_t split;              // CTAs of a cluster that share one tile's k (1: none)
   uint8_t a_tiled, w_tiled;
   uint8_t a_bytes, w_bytes;    // row-major scales that are not 4-byte words
@@ -241,6 +244,22 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// Shared memory to a box of a tensor; rows and columns outside it are not
+// written.  The thread that issues waits for its stores to have been read.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x,
+                                             int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   map),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 // A contiguous copy, counted on the stage's barrier (whose expected bytes
 // include it); addresses and size are multiples of 16.
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
@@ -402,20 +421,20 @@ __device__ __forceinline__ int64_t mm_start(int64_t bound) {
   return CG == 2 ? bound & ~(int64_t)127 : bound;
 }
 
-// A CTA's walk over its tiles: token tile and w tile, without a division per
-// tile.
+// A CTA's walk over its tiles without a division per tile: neighbours differ in
+// `lo`, the w tile (of transposed products, the token tile).
 struct MmWalk {
-  uint32_t tt, jt, dt, dj, n_tiles;
+  uint32_t hi, lo, d_hi, d_lo, n_lo;
   __device__ __forceinline__ MmWalk(uint32_t t0, const MmShape& sh)
-      : tt(t0 / sh.n_tiles), dt(sh.step_tokens), dj(sh.step_j), n_tiles(sh.n_tiles) {
-    jt = t0 - tt * n_tiles;
+      : hi(t0 / sh.n_lo), d_hi(sh.step_hi), d_lo(sh.step_lo), n_lo(sh.n_lo) {
+    lo = t0 - hi * n_lo;
   }
   __device__ __forceinline__ void next() {
-    tt += dt;
-    jt += dj;
-    if (jt >= n_tiles) {
-      jt -= n_tiles;
-      ++tt;
+    hi += d_hi;
+    lo += d_lo;
+    if (lo >= n_lo) {
+      lo -= n_lo;
+      ++hi;
     }
   }
 };
@@ -423,10 +442,9 @@ struct MmWalk {
 // For a converged warp: with several groups its lanes search the table
 // together, 32 entries at a time.
 template <int CG>
-__device__ __forceinline__ MmTile mm_tile(const MmWalk& at, const uint32_t* first_tile,
+__device__ __forceinline__ MmTile mm_tile(uint32_t tt, uint32_t jt, const uint32_t* first_tile,
                                           const int64_t* offs, const MmShape& sh) {
   MmTile m;
-  const uint32_t tt = at.tt;
   uint32_t lo = 0;  // the last group that starts at or before tt
   for (uint32_t span = (uint32_t)sh.groups; span > 1u;) {
     const uint32_t step = (span + 31u) / 32u, probe = threadIdx.x % 32u * step;
@@ -444,7 +462,7 @@ __device__ __forceinline__ MmTile mm_tile(const MmWalk& at, const uint32_t* firs
   const int64_t end = mm_bound(offs, m.group + 1, sh), to = end < from + sh.nt ? end : from + sh.nt;
   // (no tile of a valid table is empty; one of offsets that go down could be)
   m.tokens = from >= 0 && to > m.row0 ? (uint32_t)(to - m.row0) : 0u;
-  m.j0 = at.jt * (CG * kMmM);
+  m.j0 = jt * (CG * kMmM);
   m.product = m.group < sh.matrices && m.tokens > 0u;
   m.end = false;
   return m;
@@ -572,13 +590,20 @@ __device__ __forceinline__ void copy_scales(const ScaleSrc& s, const uint8_t* ba
 // the same tokens: each CTA copies its own 128 rows of w, half of the tokens'
 // codes and all of their scales, every part by TMA and counted on the leader's
 // barrier, and the leader's warp 1 issues for both.
+//   TR (pairs, one group, rows of out in whole 16 bytes): called with the operands
+// exchanged, so the "tokens" of these comments are columns of out and the rows
+// of w its rows.  A lane then holds 16 columns of a row and not 16 rows of a
+// column, nothing has to be turned, and a warp hands 32 x 32 of them to the copy
+// engine (65536 x 2048 x 256: 52 us, 72 without; 16384 x 4096 x 2048: 65 and 67).
+// Not for several groups, whose tiles end at any row.
 // ---------------------------------------------------------------------------
 struct MmMaps {
   CUtensorMap a, w;    // codes
   CUtensorMap as, ws;  // CG 2: tiled scales, a row per 128-row block
+  CUtensorMap out;     // TR
 };
 
-template <bool MX, int RB, int CG>
+template <bool MX, int RB, int CG, bool TR>
 __global__ void __launch_bounds__(kMmThreads, 1)
     k_matmul(const __grid_constant__ MmMaps maps, const uint8_t* __restrict__ as,
              const uint8_t* __restrict__ ws, const float* __restrict__ ag,
@@ -626,6 +651,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     tma_prefetch_map(&maps.w);
     tma_prefetch_map(&maps.a);
     if (PAIR) tma_prefetch_map(&maps.ws), tma_prefetch_map(&maps.as);
+    if (TR) tma_prefetch_map(&maps.out);
   }
   if (warp == 1) {
     if (PAIR) {
@@ -852,10 +878,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     at.parity = 1u;
     for (MmWalk t(blockIdx.x / team, sh);; t.next()) {
       MmTile m;
-      m.end = t.tt >= token_tiles;
+      m.end = t.hi >= (TR ? sh.n_tiles : token_tiles);
       OutScale scale{1.0f, 1.0f, 1.0f, true};
       if (!m.end) {
-        m = mm_tile<CG>(t, first_tile, offs, sh);
+        m = mm_tile<CG>(TR ? t.lo : t.hi, TR ? t.hi : t.lo, first_tile, offs, sh);
         if (!MX && m.product) scale = make_out_scale(ag[m.group], wg[m.group]);
       }
       if (!mm_wait(smem_u32(&posts.taken[at.at]), at.parity, &gave_up)) break;
@@ -871,6 +897,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   } else if (warp >= 4 && warp < 4u + 4u * OUT) {
     // OUT warps per 32 lanes of tensor memory, each every OUT-th 16 tokens
     const uint32_t q = warp % 4u, odd = warp / 4u - 1u;
+    // (TR: each every OUT-th 32, which it hands on row by row from 2 KB of its own.)
+    uint8_t* box = after + (warp - 4u) * kMmBox;
     // A piece of 16 tokens x 32 columns is turned as [token pair][column] words.
     uint32_t* mine = reinterpret_cast<uint32_t*>(after + (warp - 4u) * kMmTurnPiece);
     // Written out, a lane takes 8 columns of two tokens; the halves of its 32
@@ -896,7 +924,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       if (m.product) {
 #pragma unroll
         for (uint32_t i = 0; i < PIECES; ++i)
-          tmem_ld_32x16(d + c0 + 16u * OUT * i, v[i]);
+          tmem_ld_32x16(TR ? d + 32u * (odd + OUT * (i / 2u)) + 16u * (i % 2u) : d + c0 + 16u * OUT * i,
+                        v[i]);
         tmem_wait_ld();
 #pragma unroll
         for (uint32_t i = 0; i < PIECES; ++i) tmem_arrived(v[i]);
@@ -914,6 +943,31 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         for (uint32_t i = 0; i < PIECES; ++i)
 #pragma unroll
           for (int x = 0; x < 16; ++x) v[i][x] = 0u;
+      }
+      if (TR) {
+#pragma unroll
+        for (uint32_t i = 0; i + 1u < PIECES; i += 2u) {
+          const uint32_t c = 32u * (odd + OUT * (i / 2u));
+          if (c >= m.tokens) break;
+          uint32_t w[16];
+          scaled_bf16<MX>(v[i], scale, w);
+          scaled_bf16<MX>(v[i + 1u], scale, w + 8);
+          if (elect_one()) bulk_wait_read();  // what was handed on from this box
+          __syncwarp();
+          // the four parts of a row in the order of the 64-byte swizzle
+#pragma unroll
+          for (uint32_t x = 0; x < 4u; ++x)
+            *reinterpret_cast<uint4*>(box + lane * 64u + ((x ^ (lane / 2u % 4u)) * 16u)) =
+                make_uint4(w[4u * x], w[4u * x + 1u], w[4u * x + 2u], w[4u * x + 3u]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          // rows and columns past the last are not written
+          if (elect_one() && (int64_t)j0 < sh.n) {
+            tma_store_2d(&maps.out, smem_u32(box), (int32_t)m.row0 + (int32_t)c, (int32_t)j0);
+            bulk_commit();
+          }
+        }
+        continue;
       }
 #pragma unroll
       for (uint32_t i = 0; i < PIECES; ++i) {
@@ -956,6 +1010,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
       }
     }
+    if (TR && elect_one()) bulk_wait_read();  // shared memory outlives its readers
   }
   if (sh.split > 1u) {
     // Every CTA of the cluster holds a part of the sums of one tile; each adds

@@ -347,6 +347,26 @@ int code_map(CUtensorMap* map, const uint8_t* codes, uint64_t rows, uint64_t byt
              : TRACE_ERR_CUDA;
 }
 
+// [rows, n] bf16, stored in boxes of 32 x 32 (64-byte swizzle).
+int out_map(CUtensorMap* map, uint16_t* out, uint64_t rows, uint64_t n) {
+  const EncodeTiled encode = encode_tiled();
+  if (encode == nullptr) return TRACE_ERR_CUDA;
+  const cuuint64_t dims[2] = {n, rows}, strides[1] = {2 * n};
+  const cuuint32_t box[2] = {32, 32}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (void*)out, dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? TRACE_OK
+             : TRACE_ERR_CUDA;
+}
+
+template <typename T>
+void exchange(T* a, T* b) {
+  const T t = *a;
+  *a = *b;
+  *b = t;
+}
+
 // Tiled scales as rows of 8-byte words, one row per 128-row block, copied in
 // boxes of `atoms` 512-byte pieces.
 int scale_map(CUtensorMap* map, const uint8_t* scales, uint64_t rows, uint32_t scols,
@@ -409,8 +429,6 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   const int sms = sm_count();
   if (sms <= 0) return TRACE_ERR_CUDA;
   MmShape sh;
-  sh.rows = rows;
-  sh.n = n;
   sh.cols = (uint32_t)cols;
   sh.scols = (uint32_t)(cols / (MX ? 32 : 16));
   sh.groups = groups;
@@ -425,12 +443,12 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   sh.w_tiled = w_layout == TRACE_SCALES_TILED_128x4;
   sh.a_bytes = !sh.a_tiled && (sh.scols % 4 != 0 || !aligned(a_scales, 4));
   sh.w_bytes = !sh.w_tiled && (sh.scols % 4 != 0 || !aligned(w_scales, 4));
-  sh.w_blocks = (uint32_t)((n + 127) / 128);
   const bool pair = plan.pairs && (ws != nullptr || (!plan.retile_a && !plan.retile_w));
   if (pair && (plan.retile_a || plan.retile_w)) {
     const uint64_t runs = ((sh.scols + 3u) / 4u + 15u) / 16u;
     RetileSrc a{a_scales, ws, rows, (uint32_t)((rows + 127) / 128), 0, sh.a_tiled, sh.a_bytes};
-    RetileSrc w{w_scales, ws + plan.a_bytes, n, sh.w_blocks, 0, sh.w_tiled, sh.w_bytes};
+    RetileSrc w{w_scales, ws + plan.a_bytes, n, (uint32_t)((n + 127) / 128), 0, sh.w_tiled,
+                sh.w_bytes};
     const uint64_t a_ctas = plan.retile_a ? a.blocks * runs : 0;
     const uint64_t w_ctas = plan.retile_w ? (uint64_t)w.blocks * matrices * runs : 0;
     if (a_ctas + w_ctas > 0x7FFFFFFFu) return TRACE_ERR_SHAPE;
@@ -441,6 +459,17 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
     if (plan.retile_a) a_scales = a.dst;
     if (plan.retile_w) w_scales = w.dst;
   }
+  // out transposed, see k_matmul: (scales are all tiled by now)
+  const bool tr = pair && groups == 1 && n % 8 == 0;
+  if (tr) {
+    exchange(&a_codes, &w_codes);
+    exchange(&a_scales, &w_scales);
+    exchange(&a_gscale, &w_gscale);
+    exchange(&rows, &n);
+  }
+  sh.rows = rows;
+  sh.n = n;
+  sh.w_blocks = (uint32_t)((n + 127) / 128);
   const uint32_t cg = pair ? 2 : 1;
   sh.n_tiles = (uint32_t)((n + cg * kMmM - 1) / (cg * kMmM));
   // Tiles of 256 tokens, or of 128 where those still all run at once (512 x 4096
@@ -452,7 +481,7 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   const uint32_t rb = pair ? 2 : (sh.nt + 127) / 128;
   const uint32_t stage =
       ((kMmM + sh.nt / cg) * kMmStageBytes + kAtoms * 512u * (1 + rb) + 1023u) & ~1023u;
-  const uint32_t fixed = 1024u + kMmTurnBytes + 4u * (uint32_t)(groups + 1);
+  const uint32_t fixed = 1024u + (tr ? 12 * kMmBox : kMmTurnBytes) + 4u * (uint32_t)(groups + 1);
   sh.stages = (kSmem - 1024u - fixed) / stage;
   if (sh.stages > (uint32_t)kMmMaxStages) sh.stages = kMmMaxStages;
   sh.sf_slots = (kMmTmemCols - sh.accs * ((sh.nt + 31u) & ~31u)) / (4u * kAtoms * (1 + rb));
@@ -470,6 +499,7 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   int st = code_map(&maps.a, a_codes, (uint64_t)rows, (uint64_t)cols / 2,
                     pair ? kMmPairBox : sh.nt);
   if (!st) st = code_map(&maps.w, w_codes, (uint64_t)n * matrices, (uint64_t)cols / 2, kMmM);
+  if (!st && tr) st = out_map(&maps.out, out, (uint64_t)n, (uint64_t)rows);
   if (!st && pair) st = scale_map(&maps.as, a_scales, (uint64_t)rows, sh.scols, kAtoms);
   if (!st && pair) st = scale_map(&maps.ws, w_scales, (uint64_t)sh.w_blocks * matrices * 128u, sh.scols, kAtoms);
   if (st) return st;
@@ -477,11 +507,13 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TRACE_ERR_CUDA;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(k_matmul<MX, 1, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(k_matmul<MX, 1, 1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kSmem - 1024u)) != cudaSuccess ||
-        cudaFuncSetAttribute(k_matmul<MX, 2, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(k_matmul<MX, 2, 1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kSmem - 1024u)) != cudaSuccess ||
-        cudaFuncSetAttribute(k_matmul<MX, 2, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(k_matmul<MX, 2, 2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kSmem - 1024u)) != cudaSuccess ||
+        cudaFuncSetAttribute(k_matmul<MX, 2, 2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kSmem - 1024u)) != cudaSuccess)
       return TRACE_ERR_CUDA;
     attr_set[dev] = true;
@@ -490,8 +522,9 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   const uint32_t team = pair ? 2 : sh.split;  // CTAs of a cluster
   uint32_t teams = (uint32_t)sms / team;
   if (groups == 1 && tiles < teams) teams = (uint32_t)tiles;
-  sh.step_tokens = teams / sh.n_tiles;
-  sh.step_j = teams % sh.n_tiles;
+  sh.n_lo = tr ? (uint32_t)((rows + sh.nt - 1) / sh.nt) : sh.n_tiles;
+  sh.step_hi = teams / sh.n_lo;
+  sh.step_lo = teams % sh.n_lo;
   cfg.gridDim = dim3(team * teams);
   cfg.blockDim = dim3(kMmThreads);
   cfg.dynamicSmemBytes = sh.stages * stage + fixed;
@@ -505,9 +538,10 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg,
-                            pair      ? k_matmul<MX, 2, 2>
-                            : rb == 1 ? k_matmul<MX, 1, 1>
-                                      : k_matmul<MX, 2, 1>,
+                            tr        ? k_matmul<MX, 2, 2, true>
+                            : pair    ? k_matmul<MX, 2, 2, false>
+                            : rb == 1 ? k_matmul<MX, 1, 1, false>
+                                      : k_matmul<MX, 2, 1, false>,
                             maps, a_scales, w_scales, a_gscale, w_gscale,
                             groups > 1 ? offs : (const int64_t*)nullptr, sh, out) == cudaSuccess
              ? TRACE_OK
