@@ -943,6 +943,13 @@ def moe_combine_bwd(grad: torch.Tensor, y: torch.Tensor, route: MoeRoute, weight
     return grad_y, grad_w
 
 
+def _upstream(grad: torch.Tensor) -> torch.Tensor:
+    """A gradient as the kernels read it: contiguous, and moved if it is a part
+    of a larger one that starts at an odd address."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 32 == 0 else grad.clone()
+
+
 class MoeDispatch(torch.autograd.Function):
     """Autograd wrapper of the dispatch; both directions run in the library."""
 
@@ -954,7 +961,7 @@ class MoeDispatch(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        return moe_dispatch_bwd(grad.contiguous(), MoeRoute(*ctx.saved_tensors)), None
+        return moe_dispatch_bwd(_upstream(grad), MoeRoute(*ctx.saved_tensors)), None
 
 
 class MoeCombine(torch.autograd.Function):
@@ -969,7 +976,7 @@ class MoeCombine(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         y, weights, *route = ctx.saved_tensors
-        grad_y, grad_w = moe_combine_bwd(grad.contiguous(), y, MoeRoute(*route), weights)
+        grad_y, grad_w = moe_combine_bwd(_upstream(grad), y, MoeRoute(*route), weights)
         return grad_y, None, grad_w
 
 

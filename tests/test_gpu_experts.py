@@ -765,3 +765,22 @@ def test_product_of_pairs_in_several_waves(fmt, rows, n, cols):
     more of them than others."""
     assert -(-rows // 128) * -(-n // 256) > torch.cuda.get_device_properties(0).multi_processor_count // 2
     _product_case(rows, n, cols, fmt, True, True, seed=rows + n)
+
+
+def test_gradients_that_start_anywhere():
+    """A part of a larger gradient is contiguous and yet not 32-byte aligned."""
+    tokens, k, cols = 11, 2, 64
+    route, _ = _route(tokens, k, 3, 7)
+    g = _gen(8)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g).bfloat16().to(DEV)  # noqa: E731
+    x, y, w = ints(tokens, cols), ints(tokens * k, cols), ints(tokens, k).float()
+    head, up = ints(5), ints(5 + tokens * k * cols)
+    x.requires_grad_(), y.requires_grad_(), w.requires_grad_()
+    flat = torch.cat((head, ops.moe_dispatch(x, route).view(-1)))
+    (dx,) = torch.autograd.grad(flat, x, up)
+    assert torch.equal(dx, ops.moe_dispatch_bwd(up[5:].clone().view(-1, cols), route))
+    flat = torch.cat((head, ops.moe_combine(y, route, w).view(-1)))
+    part = up[:5 + tokens * cols]
+    dy, dw = torch.autograd.grad(flat, (y, w), part)
+    want = ops.moe_combine_bwd(part[5:].clone().view(tokens, cols), y.detach(), route, w.detach())
+    assert torch.equal(dy, want[0]) and torch.equal(dw, want[1])
