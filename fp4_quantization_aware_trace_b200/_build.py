@@ -1,4 +1,5 @@
-"""Build libtrace_fp4.so in-tree with nvcc for sm_100a (no torch involved)."""
+"""Build libtrace_fp4.so in-tree with nvcc for sm_100a (no torch involved), and
+the Python module beside it that calls it for torch tensors (g++)."""
 from __future__ import annotations
 
 import os
@@ -9,6 +10,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "trace_fp4.cu")
 CSRC_DIR = os.path.join(PKG, "csrc")
+BIND_SRC = os.path.join(PKG, "csrc", "binding.cpp")
+BIND = os.path.join(PKG, "_binding.so")
 HDR = os.path.join(ROOT, "include", "trace_fp4.h")
 LIB = os.path.join(PKG, "libtrace_fp4.so")
 
@@ -31,7 +34,9 @@ def nvcc() -> str:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/trace_fp4.cu (which includes the csrc/*.cuh kernels) into
-    the package directory; returns the path."""
+    the package directory, and the Python module beside it; returns the
+    library's path."""
+    build_binding(force)
     deps = [HDR] + [os.path.join(CSRC_DIR, f) for f in os.listdir(CSRC_DIR)
                     if f.endswith((".cu", ".cuh"))]
     if (not force and os.path.exists(LIB)
@@ -51,6 +56,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.cpp against the installed torch; returns the path."""
+    if (not force and os.path.exists(BIND)
+            and os.path.getmtime(BIND) >= max(os.path.getmtime(d) for d in (HDR, BIND_SRC))):
+        return BIND
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_path("include"),
+           "-isystem", os.path.join(t, "include"),
+           "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-o", tmp, BIND_SRC,
+           "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+           "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed building _binding.so")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 if __name__ == "__main__":
     build(force=True, verbose="-v" in sys.argv)
-    print(LIB)
+    print(LIB, BIND)

@@ -766,6 +766,28 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+_bind = None
+
+
+def binding():
+    """The module that makes the usual call of an expert operator in one native
+    step (csrc/binding.cpp); each of its functions returns None for any other
+    call.  Raises if it has not been built."""
+    global _bind
+    if _bind is None:
+        lib = library()
+        with _lock:
+            if not os.path.exists(os.path.join(_PKG, "_binding.so")):
+                raise TraceError(f"{_PKG}/_binding.so is missing: it has not been built")
+            from . import _binding
+            _binding.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.trace_moe_sort, lib.trace_moe_sort_workspace_bytes, lib.trace_moe_dispatch,
+                lib.trace_moe_combine, lib.trace_moe_combine_bwd, lib.trace_fp4_matmul,
+                lib.trace_mx_matmul, lib.trace_fp4_matmul_workspace_bytes, lib.trace_mx_matmul_workspace_bytes)))
+            _bind = _binding
+    return _bind
+
+
 class _On:
     """Work on the tensors' own device and on `stream` (default: that
     device's current stream), so that outputs are allocated there too; gives
@@ -835,38 +857,33 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, out: MoeRoute | None = 
              workspace: torch.Tensor | None = None, stream=None) -> MoeRoute:
     """Stable sort of the slots of expert_ids (int32 / int64 [tokens, k]) by
     expert; ids outside [0, num_experts) drop their slot."""
+    if out is None and workspace is None and stream is None:
+        got = (_bind or binding()).sort(expert_ids, num_experts)
+        if got is not None:
+            return MoeRoute(*got)
     if expert_ids.dim() != 2 or expert_ids.shape[1] < 1:
         raise TraceError("expert ids must be [tokens, k]")
     _want(expert_ids, "expert ids", (torch.int32, torch.int64))
     tokens, k = expert_ids.shape
-    lib, base = library(), None
+    lib = library()
     nbytes = trace_moe_sort_workspace_bytes(tokens, k, num_experts)
     if nbytes == 0:
         raise TraceError(f"moe_sort: {num_experts} experts for [{tokens}, {k}] ids")
     with _On(stream, expert_ids, workspace) as s:
         if out is None:
-            # one allocation: workspace, offsets, rows, slots (the workspace a
-            # multiple of 256 bytes, so each part is aligned)
-            own = 0 if workspace is not None else nbytes // 8
-            at, slots = own + num_experts + 2, tokens * k
-            base = expert_ids.new_empty(at + slots, dtype=torch.int64)
-            words = base.view(torch.int32)
-            out = MoeRoute(torch.as_strided(base, (num_experts + 2,), (1,), own),
-                           torch.as_strided(words, (tokens, k), (k, 1), 2 * at),
-                           torch.as_strided(words, (slots,), (1,), 2 * at + slots))
-            if workspace is None:
-                workspace = base
+            new = lambda *shape: expert_ids.new_empty(shape, dtype=torch.int32)  # noqa: E731
+            out = MoeRoute(expert_ids.new_empty(num_experts + 2, dtype=torch.int64), new(tokens, k),
+                           new(tokens * k))
         else:
             _want(out.offsets, "offsets", torch.int64, (num_experts + 2,))
             _want(out.rows, "rows", torch.int32, (tokens, k))
             _want(out.slots, "slots", torch.int32, (tokens * k,))
             _On(None, expert_ids, out.offsets, out.rows, out.slots)
-            if workspace is None:
-                workspace = expert_ids.new_empty(nbytes, dtype=torch.uint8)
+        if workspace is None:
+            workspace = expert_ids.new_empty(nbytes, dtype=torch.uint8)
         ids, offsets, rows, slots, ws = _ptrs(expert_ids, out.offsets, out.rows, out.slots, workspace)
         st = lib.trace_moe_sort(ids, expert_ids.element_size(), tokens, k, num_experts, offsets, rows,
-                                slots, ws, nbytes if workspace is base else
-                                workspace.numel() * workspace.element_size(), s)
+                                slots, ws, workspace.numel() * workspace.element_size(), s)
         _check(st, "trace_moe_sort")
     return out
 
@@ -983,6 +1000,9 @@ class MoeCombine(torch.autograd.Function):
 def moe_dispatch(x: torch.Tensor, route: MoeRoute) -> torch.Tensor:
     """Differentiable dispatch of tokens into expert order (for
     capture(y, route.offsets) and the grouped product)."""
+    y = (_bind or binding()).dispatch(x, route.rows, route.slots)
+    if y is not None:
+        return y
     if torch.is_grad_enabled() and x.requires_grad:
         return MoeDispatch.apply(x, route)
     return moe_dispatch_fwd(x, route)
@@ -990,6 +1010,9 @@ def moe_dispatch(x: torch.Tensor, route: MoeRoute) -> torch.Tensor:
 
 def moe_combine(y: torch.Tensor, route: MoeRoute, weights: torch.Tensor) -> torch.Tensor:
     """Differentiable return to token order, weighted by the router."""
+    out = (_bind or binding()).combine(y, route.rows, route.slots, weights)
+    if out is not None:
+        return out
     if torch.is_grad_enabled() and (y.requires_grad or weights.requires_grad):
         return MoeCombine.apply(y, route, weights)
     return moe_combine_fwd(y, route, weights)
@@ -1031,6 +1054,12 @@ def _matmul(a, w, cols, offsets, matrices, out, workspace, stream, bs):
         cols = s.shape[1] * bs
     if cols <= 0 or cols % 32:
         raise TraceError(f"cols must be a multiple of 32: {cols}")
+    if out is None and workspace is None and stream is None and not (DEBUG and offsets is not None):
+        got = (_bind or binding()).matmul(bs, cols, matrices, offsets, a.codes, a.scales,
+                                          a.gscale if bs == 16 else None, w.codes, w.scales,
+                                          w.gscale if bs == 16 else None)
+        if got is not None:
+            return got
     rows, la = _matmul_operand(a, cols, bs, "a")
     wrows, lw = _matmul_operand(w, cols, bs, "w")
     groups = _groups(offsets, rows)

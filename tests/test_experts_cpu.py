@@ -129,3 +129,22 @@ def test_product_workspace(lib):
         assert lib.trace_fp4_matmul_ws(A, A, A, *big, A, A, A, 4096, 1, 0, A, ws, n, None) == st
     assert lib.trace_mx_matmul_ws(A, A, *big, A, A, 4096, 1, 0, A, A, 48 * 32 * 512 - 1, None) == 4
     assert lib.trace_fp4_matmul_ws(A, A, A, 4, 48, 1, None, 0, A, A, A, 8, 1, 0, A, A, 0, None) == 2
+
+
+def test_native_calls_leave_the_unusual(lib):
+    """None, and nothing asked of CUDA, for host tensors, other objects and
+    other numbers of arguments."""
+    b = ops.binding()
+    i, h = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 32).bfloat16()
+    u = torch.zeros(64, dtype=torch.uint8)
+    for args in [(i, 4), (i, 4.5), (None, 4), ()]:
+        assert b.sort(*args) is None
+    for args in [(h, i, i.view(-1)), (1, 2, 3), (h,)]:
+        assert b.dispatch(*args) is None
+    for args in [(h, i, i.view(-1), torch.zeros(3, 2)), (None,) * 4, ()]:
+        assert b.combine(*args) is None
+    for args in [(16, 32, 1, None, u, u, None, u, u, None), (16, 0, 1, None, u, u, None, u, u, None),
+                 (32, 1 << 80, 1, None, u, u, None, u, u, None), (8, 32, "x", *([None] * 7)), ()]:
+        assert b.matmul(*args) is None
+    with pytest.raises(TypeError):
+        b.setup(1)

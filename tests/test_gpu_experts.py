@@ -767,6 +767,57 @@ def test_product_of_pairs_in_several_waves(fmt, rows, n, cols):
     _product_case(rows, n, cols, fmt, True, True, seed=rows + n)
 
 
+# ---------------------------------------------------------------------------
+# The two ways of a call, gradients at odd addresses, one very long sum
+# ---------------------------------------------------------------------------
+
+def _both_ways(call):
+    """The usual call, and the same on a stream that is named (never one native step)."""
+    s = torch.cuda.current_stream()
+    return call(), call(stream=s)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tiled", [False, True])
+def test_both_ways_of_a_product(fmt, tiled):
+    g = _gen(3)
+    x = torch.randn(70, 320, generator=g).bfloat16().to(DEV)
+    w = torch.randn(3 * 48, 320, generator=g).bfloat16().to(DEV)
+    offs = torch.tensor([0, 30, 30, 61, 70], device=DEV)
+    for experts, o in ((1, None), (3, offs)):
+        bounds = None if experts == 1 else torch.arange(0, 145, 48, device=DEV)
+        a, b = _capture(x, fmt, tiled, o), _capture(w, fmt, tiled, bounds)
+        if fmt == "nvfp4":
+            one, two = _both_ways(lambda **k: ops.fp4_matmul(a, b, 320, **k))
+        else:
+            one, two = _both_ways(lambda **k: ops.mx_matmul(a, b, 320, o, experts, **k))
+        assert one.shape == (70, 144 // experts) and torch.equal(one, two)
+
+
+def test_both_ways_of_sort_dispatch_and_combine():
+    g = _gen(6)
+    for dtype in (torch.int32, torch.int64):
+        ids = torch.randint(-1, 9, (77, 3), generator=g).to(dtype).to(DEV)
+        one, two = _both_ways(lambda **k: ops.moe_sort(ids, 8, **k))
+        for u, v in zip((one.offsets, one.rows, one.slots), (two.offsets, two.rows, two.slots)):
+            assert u.dtype == v.dtype and torch.equal(u, v)
+    x = torch.randn(77, 96, generator=g).bfloat16().to(DEV)
+    w = torch.rand(77, 3, generator=g).to(DEV)
+    y = ops.moe_dispatch(x, one)
+    assert torch.equal(y, ops.moe_dispatch_fwd(x, one))
+    assert torch.equal(ops.moe_combine(y, one, w), ops.moe_combine_fwd(y, one, w))
+    with torch.no_grad():  # a leaf, but nothing to differentiate
+        assert not ops.moe_dispatch(x.requires_grad_(), one).requires_grad
+    assert ops.moe_dispatch(x, one).requires_grad
+
+
+def test_a_route_can_be_saved(tmp_path):
+    route, _ = _route(9, 2, 4, 5)
+    torch.save((route.offsets, route.rows, route.slots), tmp_path / "route.pt")
+    for u, v in zip(torch.load(tmp_path / "route.pt"), (route.offsets, route.rows, route.slots)):
+        assert torch.equal(u, v)
+
+
 def test_gradients_that_start_anywhere():
     """A part of a larger gradient is contiguous and yet not 32-byte aligned."""
     tokens, k, cols = 11, 2, 64
@@ -784,3 +835,19 @@ def test_gradients_that_start_anywhere():
     dy, dw = torch.autograd.grad(flat, (y, w), part)
     want = ops.moe_combine_bwd(part[5:].clone().view(tokens, cols), y.detach(), route, w.detach())
     assert torch.equal(dy, want[0]) and torch.equal(dw, want[1])
+
+
+@pytest.mark.parametrize("groups", [1, 2])
+def test_product_of_the_longest_rows(groups):
+    """2^31 - 1024 terms to a sum, of which the first and the last 2^20 are one
+    and the others zero: exact in fp32, in which it is held, and in bf16."""
+    cols, ones = (1 << 31) - 1024, 1 << 19
+    codes = torch.zeros(groups, cols // 2, dtype=torch.uint8, device=DEV)
+    codes[:, :ones] = codes[:, -ones:] = 0x22
+    scales = torch.full((groups, cols // 16), 0x38, dtype=torch.uint8, device=DEV)
+    offs = None if groups == 1 else torch.arange(groups + 1, device=DEV)
+    unit = torch.ones(groups, device=DEV)
+    a = ops.Capture(codes.view(-1), None, scales, unit, offs)
+    assert ops.matmul_status()
+    out = ops.fp4_matmul(a, ops.Capture(a.codes, None, a.scales, unit))
+    assert ops.matmul_status() and out.flatten().tolist() == [2.0 ** 21] * groups
