@@ -73,67 +73,81 @@ __device__ __forceinline__ uint32_t same_key(uint32_t key, uint32_t bits) {
 // then become each warp's next row per expert: rows of earlier experts +
 // this expert's rows in earlier chunks + in earlier warps.  In the last
 // walk the lanes of one expert rank themselves by lane, which is slot order.
-// Bound by latencies, so a warp reads an expert's counts of all chunks at once
-// (65536 x 8 slots, 128 experts: 18 us for both passes; with a thread per
-// expert that walked its counts, and the match instruction, 26 us).
+// Bound by latencies, so what does not depend on one another is asked for
+// together: a warp's keys, and the counts of all chunks of five experts; and the
+// warps' counters of an expert are scanned by a warp, not by a thread (65536 x 8
+// slots, 128 experts: 12.8 us for both passes; 17.4 us with the counts of one
+// expert at a time and a thread for each expert's counters).
+constexpr uint32_t kSortAtOnce = 5u;  // experts of a warp whose counts are read together
 template <typename ID>
 __global__ void __launch_bounds__(32 * kSortMaxWarps)
     k_moe_place(const ID* __restrict__ ids, uint32_t slots, uint32_t chunk, uint32_t E,
                 const uint32_t* __restrict__ counts, int64_t* __restrict__ offsets,
                 int32_t* __restrict__ rows, int32_t* __restrict__ slot_of) {
-  extern __shared__ uint32_t next[];  // [warps][E + 1], all[E + 1], earlier[E + 1]
+  extern __shared__ uint32_t next[];  // [warps][stride], all[E + 1], earlier[E + 1]
   __shared__ uint32_t part[kSortMaxWarps];
   __shared__ uint32_t carry;
-  const uint32_t n = E + 1u, warps = blockDim.x / 32u;
+  const uint32_t n = E + 1u, stride = n | 1u, warps = blockDim.x / 32u;
   const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
-  uint32_t* all = next + warps * n;
+  uint32_t* all = next + warps * stride;
   uint32_t* earlier = all + n;
-  pdl_begin();
-  for (uint32_t i = threadIdx.x; i < warps * n; i += blockDim.x) next[i] = 0u;
-  if (threadIdx.x == 0) carry = 0u;
-  if (counts != nullptr)
-    for (uint32_t e = warp; e < n; e += warps) {
-      uint32_t total = 0u, before = 0u;
-      uint32_t v[kSortMaxChunks / 32u];  // all on their way at once
-#pragma unroll
-      for (uint32_t i = 0; i < kSortMaxChunks / 32u; ++i) {
-        const uint32_t c = lane + 32u * i;
-        v[i] = c < gridDim.x ? counts[(size_t)e * gridDim.x + c] : 0u;
-      }
-#pragma unroll
-      for (uint32_t i = 0; i < kSortMaxChunks / 32u; ++i) {
-        total += v[i];
-        before += lane + 32u * i < blockIdx.x ? v[i] : 0u;
-      }
-      total = __reduce_add_sync(0xFFFFFFFFu, total);
-      before = __reduce_add_sync(0xFFFFFFFFu, before);
-      if (lane == 0) all[e] = total, earlier[e] = before;
-    }
-  __syncthreads();
   const uint32_t first = blockIdx.x * chunk, last = min(first + chunk, slots);
   const uint32_t piece = (last - first + warps * 32u - 1u) / (warps * 32u) * 32u;
   const uint32_t lo = min(first + warp * piece, last), hi = min(lo + piece, last);
-  uint32_t* mine = next + warp * n;
+  const bool once = hi - lo <= 128u;  // all of the warp's keys are held
+  pdl_begin();
   uint32_t key[4];
+  sort_keys(ids, lo, hi, E, n, key);
+  for (uint32_t i = threadIdx.x; i < warps * stride; i += blockDim.x) next[i] = 0u;
+  if (threadIdx.x == 0) carry = 0u;
+  if (counts != nullptr)
+    for (uint32_t e0 = warp; e0 < n; e0 += kSortAtOnce * warps) {
+      uint32_t total[kSortAtOnce] = {}, before[kSortAtOnce] = {};
+      for (uint32_t c0 = 0; c0 < gridDim.x; c0 += 128u) {
+        uint32_t v[kSortAtOnce][4];
+#pragma unroll
+        for (uint32_t x = 0; x < kSortAtOnce; ++x)
+#pragma unroll
+          for (uint32_t i = 0; i < 4u; ++i) {
+            const uint32_t e = e0 + x * warps, c = c0 + lane + 32u * i;
+            v[x][i] = e < n && c < gridDim.x ? counts[(size_t)e * gridDim.x + c] : 0u;
+          }
+#pragma unroll
+        for (uint32_t x = 0; x < kSortAtOnce; ++x)
+#pragma unroll
+          for (uint32_t i = 0; i < 4u; ++i) {
+            total[x] += v[x][i];
+            before[x] += c0 + lane + 32u * i < blockIdx.x ? v[x][i] : 0u;
+          }
+      }
+#pragma unroll
+      for (uint32_t x = 0; x < kSortAtOnce; ++x) {
+        const uint32_t t = __reduce_add_sync(0xFFFFFFFFu, total[x]);
+        const uint32_t u = __reduce_add_sync(0xFFFFFFFFu, before[x]);
+        if (lane == 0 && e0 + x * warps < n) all[e0 + x * warps] = t, earlier[e0 + x * warps] = u;
+      }
+    }
+  __syncthreads();
+  uint32_t* mine = next + warp * stride;
   for (uint32_t s0 = lo; s0 < hi; s0 += 128u) {
-    sort_keys(ids, s0, hi, E, n, key);
+    if (!once) sort_keys(ids, s0, hi, E, n, key);
 #pragma unroll
     for (uint32_t i = 0; i < 4u; ++i)
       if (key[i] < n) atomicAdd(&mine[key[i]], 1u);
   }
   __syncthreads();
-  for (uint32_t e0 = 0; e0 < n; e0 += blockDim.x) {
-    const uint32_t e = e0 + threadIdx.x;
-    uint32_t total = 0u, before = 0u;
-    if (e < n) {
-      if (counts != nullptr) {
-        total = all[e];
-        before = earlier[e];
-      } else {
-        for (uint32_t w = 0; w < warps; ++w) total += next[w * n + e];
-      }
+  if (counts == nullptr) {  // this CTA's counts are all there are
+    for (uint32_t e = threadIdx.x; e < n; e += blockDim.x) earlier[e] = 0u;
+    for (uint32_t e = warp; e < n; e += warps) {
+      const uint32_t t = __reduce_add_sync(0xFFFFFFFFu, lane < warps ? next[lane * stride + e] : 0u);
+      if (lane == 0) all[e] = t;
     }
-    // exclusive scan of the totals over the CTA
+    __syncthreads();
+  }
+  // exclusive scan of the totals over the CTA: earlier[e] becomes the chunk's
+  // first row of expert e
+  for (uint32_t e0 = 0; e0 < n; e0 += blockDim.x) {
+    const uint32_t e = e0 + threadIdx.x, total = e < n ? all[e] : 0u;
     uint32_t sum = total;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -142,25 +156,30 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps)
     }
     if (lane == 31u) part[warp] = sum;
     __syncthreads();
-    uint32_t base = carry;
-    for (uint32_t w = 0; w < warp; ++w) base += part[w];
-    uint32_t at = base + sum - total;
+    const uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? part[lane] : 0u);
+    const uint32_t at = carry + before + sum - total;
     __syncthreads();
-    if (threadIdx.x == blockDim.x - 1u) carry = base + sum;
+    if (threadIdx.x == blockDim.x - 1u) carry = at + total;
     if (e < n) {
       if (blockIdx.x == 0) offsets[e] = (int64_t)at;
-      at += before;
-      for (uint32_t w = 0; w < warps; ++w) {
-        const uint32_t v = next[w * n + e];
-        next[w * n + e] = at;
-        at += v;
-      }
+      earlier[e] += at;
     }
     __syncthreads();
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) offsets[n] = (int64_t)slots;
+  // of each expert the warps' counters, a lane each
+  for (uint32_t e = warp; e < n; e += warps) {
+    const uint32_t v = lane < warps ? next[lane * stride + e] : 0u;
+    uint32_t sum = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= (uint32_t)d) sum += u;
+    }
+    if (lane < warps) next[lane * stride + e] = earlier[e] + sum - v;
+  }
+  __syncthreads();
   const uint32_t bits = 32u - (uint32_t)__clz((int)n);
-  const bool once = hi - lo <= 128u;  // the keys are still here
   for (uint32_t s0 = lo; s0 < hi; s0 += 128u) {
     if (!once) sort_keys(ids, s0, hi, E, n, key);
 #pragma unroll

@@ -277,7 +277,7 @@ template <typename ID>
 int moe_sort_launch(const ID* ids, uint32_t slots, uint32_t E, int64_t* offsets,
                     int32_t* rows, int32_t* slot_of, uint32_t* counts, cudaStream_t s) {
   const uint32_t chunk = sort_chunk(slots), chunks = (slots + chunk - 1) / chunk;
-  uint32_t warps = kSortSmem / (4u * (E + 1u)) - 2u;
+  uint32_t warps = kSortSmem / (4u * ((E + 1u) | 1u)) - 2u;
   static bool attr_set[kMaxDevices];  // benign race: same value
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TRACE_ERR_CUDA;
@@ -303,7 +303,7 @@ int moe_sort_launch(const ID* ids, uint32_t slots, uint32_t E, int64_t* offsets,
       return TRACE_ERR_CUDA;
   }
   cfg.blockDim = dim3(32u * warps);
-  cfg.dynamicSmemBytes = 4u * (warps + 2u) * (E + 1u);
+  cfg.dynamicSmemBytes = 4u * (warps + 2u) * ((E + 1u) | 1u);
   return cudaLaunchKernelEx(&cfg, k_moe_place<ID>, ids, slots, chunk, E,
                             (const uint32_t*)(chunks > 1 ? counts : nullptr), offsets, rows,
                             slot_of) == cudaSuccess
