@@ -80,7 +80,6 @@ struct MmShape {
   uint32_t split;              // CTAs of a cluster that share one tile's k (1: none)
   uint8_t a_tiled, w_tiled;
   uint8_t a_bytes, w_bytes;    // row-major scales that are not 4-byte words
-  uint8_t out16;               // rows of out are 16-byte aligned
 };
 
 __device__ uint32_t g_matmul_gave_up;  // set if a wait ran out of polls
@@ -596,6 +595,13 @@ __device__ __forceinline__ void copy_scales(const ScaleSrc& s, const uint8_t* ba
 // column, nothing has to be turned, and a warp hands 32 x 32 of them to the copy
 // engine (65536 x 2048 x 256: 52 us, 72 without; 16384 x 4096 x 2048: 65 and 67).
 // Not for several groups, whose tiles end at any row.
+//   W16: rows of out are whole 16 bytes.  Others are written in words of two
+// columns where a piece is whole and k is not long, else one column at a time.
+// That is bound by the instructions (45231 x n x 224, 4 experts: 104 us with n =
+// 2446 and 117 with 2447, 67 with 2448; one column at a time 136.  65536 x 1534 x
+// 2048, 32 experts: 128 and 140; 4099 x 4001 x 4096, where the stores come beside
+// the next tile's products: 37.6 and 36.6).  Kernels of their own, because the
+// registers of both would not fit one.
 // ---------------------------------------------------------------------------
 struct MmMaps {
   CUtensorMap a, w;    // codes
@@ -603,7 +609,7 @@ struct MmMaps {
   CUtensorMap out;     // TR
 };
 
-template <bool MX, int RB, int CG, bool TR>
+template <bool MX, int RB, int CG, bool TR, bool W16>
 __global__ void __launch_bounds__(kMmThreads, 1)
     k_matmul(const __grid_constant__ MmMaps maps, const uint8_t* __restrict__ as,
              const uint8_t* __restrict__ ws, const float* __restrict__ ag,
@@ -986,27 +992,51 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 #pragma unroll
         for (uint32_t x = 0; x < 8u; ++x) mine[32u * x + lane] = w[x];
         __syncwarp();
-        if (sh.out16) {
-          const uint4 a = *reinterpret_cast<const uint4*>(mine + 32u * pair + col + flip);
-          const uint4 b = *reinterpret_cast<const uint4*>(mine + 32u * pair + col + (4u - flip));
-          const uint4 lo = flip ? b : a, hi = flip ? a : b;  // columns + 0..3 and + 4..7
-          const uint32_t row = c + 2u * pair;
-          if ((int64_t)j0 + col < sh.n) {
-            uint16_t* at = to + (size_t)row * sh.n + col;
-            if (row >= m.lead && row < m.tokens)
-              *reinterpret_cast<uint4*>(at) =
-                  make_uint4(__byte_perm(lo.x, lo.y, 0x5410), __byte_perm(lo.z, lo.w, 0x5410),
-                             __byte_perm(hi.x, hi.y, 0x5410), __byte_perm(hi.z, hi.w, 0x5410));
-            if (row + 1u >= m.lead && row + 1u < m.tokens)
-              *reinterpret_cast<uint4*>(at + sh.n) =
-                  make_uint4(__byte_perm(lo.x, lo.y, 0x7632), __byte_perm(lo.z, lo.w, 0x7632),
-                             __byte_perm(hi.x, hi.y, 0x7632), __byte_perm(hi.z, hi.w, 0x7632));
+        if (!W16 && sh.cols <= 2048u && m.lead <= c && c + 16u <= m.tokens &&
+            (int64_t)j0 + 32 <= sh.n) {
+          // Words of two columns, a token by each half of the warp.  In a row at an
+          // odd element they begin with the second column; its first and last
+          // columns follow by themselves.
+          const uint32_t half = lane / 16u;
+          const uint32_t x = 2u * (lane % 16u) + ((uint32_t)sh.n & ((uint32_t)m.row0 + c + half) & 1u);
+          const uint32_t *lo = mine + x, *hi = mine + min(x + 1u, 31u), sel = half ? 0x7632u : 0x5410u;
+          uint32_t v2[8];
+#pragma unroll
+          for (uint32_t p = 0; p < 8u; ++p) v2[p] = __byte_perm(lo[32u * p], hi[32u * p], sel);
+          uint16_t* at = to + (size_t)(c + half) * sh.n + x;
+          const size_t step = 2u * (size_t)sh.n;
+          if (x < 31u) {
+#pragma unroll
+            for (uint32_t p = 0; p < 8u; ++p, at += step) *reinterpret_cast<uint32_t*>(at) = v2[p];
           }
-        } else if ((int64_t)j0 + lane < sh.n) {
+          if (((uint32_t)sh.n & 1u) && (((uint32_t)m.row0 + c + lane) & 1u))
+            to[(size_t)(c + lane % 16u) * sh.n + 31u * half] =
+                (uint16_t)(mine[lane % 16u / 2u * 32u + 31u * half] >> (lane % 2u * 16u));
+          continue;
+        }
+        if (!W16) {
           const uint32_t last = min(c + 16u, m.tokens);
-          for (uint32_t row = max(c, m.lead); row < last; ++row)
-            to[(size_t)row * sh.n + lane] =
-                (uint16_t)(mine[(row - c) / 2u * 32u + lane] >> ((row - c) % 2u * 16u));
+          if ((int64_t)j0 + lane < sh.n)
+#pragma unroll 4
+            for (uint32_t row = max(c, m.lead); row < last; ++row)
+              to[(size_t)row * sh.n + lane] =
+                  (uint16_t)(mine[(row - c) / 2u * 32u + lane] >> ((row - c) % 2u * 16u));
+          continue;
+        }
+        const uint4 a = *reinterpret_cast<const uint4*>(mine + 32u * pair + col + flip);
+        const uint4 b = *reinterpret_cast<const uint4*>(mine + 32u * pair + col + (4u - flip));
+        const uint4 lo = flip ? b : a, hi = flip ? a : b;  // columns + 0..3 and + 4..7
+        const uint32_t row = c + 2u * pair;
+        if ((int64_t)j0 + col < sh.n) {
+          uint16_t* at = to + (size_t)row * sh.n + col;
+          if (row >= m.lead && row < m.tokens)
+            *reinterpret_cast<uint4*>(at) =
+                make_uint4(__byte_perm(lo.x, lo.y, 0x5410), __byte_perm(lo.z, lo.w, 0x5410),
+                           __byte_perm(hi.x, hi.y, 0x5410), __byte_perm(hi.z, hi.w, 0x5410));
+          if (row + 1u >= m.lead && row + 1u < m.tokens)
+            *reinterpret_cast<uint4*>(at + sh.n) =
+                make_uint4(__byte_perm(lo.x, lo.y, 0x7632), __byte_perm(lo.z, lo.w, 0x7632),
+                           __byte_perm(hi.x, hi.y, 0x7632), __byte_perm(hi.z, hi.w, 0x7632));
         }
       }
     }

@@ -494,7 +494,6 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   if (groups == 1 && !pair)
     while (sh.split < kMmMaxSplit && tiles * (sh.split * 2) <= 128 && sh.ksteps >= sh.split * 2)
       sh.split *= 2;
-  sh.out16 = n % 8 == 0;
   MmMaps maps;
   int st = code_map(&maps.a, a_codes, (uint64_t)rows, (uint64_t)cols / 2,
                     pair ? kMmPairBox : sh.nt);
@@ -506,16 +505,18 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   static bool attr_set[kMaxDevices];  // benign race: same value
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TRACE_ERR_CUDA;
+  using Kernel = void (*)(MmMaps, const uint8_t*, const uint8_t*, const float*, const float*,
+                          const int64_t*, MmShape, uint16_t*);
+  const Kernel kernels[7] = {
+      k_matmul<MX, 1, 1, false, false>, k_matmul<MX, 2, 1, false, false>,
+      k_matmul<MX, 2, 2, false, false>, k_matmul<MX, 1, 1, false, true>,
+      k_matmul<MX, 2, 1, false, true>,  k_matmul<MX, 2, 2, false, true>,
+      k_matmul<MX, 2, 2, true, true>};
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(k_matmul<MX, 1, 1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kSmem - 1024u)) != cudaSuccess ||
-        cudaFuncSetAttribute(k_matmul<MX, 2, 1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kSmem - 1024u)) != cudaSuccess ||
-        cudaFuncSetAttribute(k_matmul<MX, 2, 2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kSmem - 1024u)) != cudaSuccess ||
-        cudaFuncSetAttribute(k_matmul<MX, 2, 2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kSmem - 1024u)) != cudaSuccess)
-      return TRACE_ERR_CUDA;
+    for (const Kernel k : kernels)
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)(kSmem - 1024u)) != cudaSuccess)
+        return TRACE_ERR_CUDA;
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
@@ -537,11 +538,8 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg,
-                            tr        ? k_matmul<MX, 2, 2, true>
-                            : pair    ? k_matmul<MX, 2, 2, false>
-                            : rb == 1 ? k_matmul<MX, 1, 1, false>
-                                      : k_matmul<MX, 2, 1, false>,
+  const int which = tr ? 6 : (pair ? 2 : rb == 1 ? 0 : 1) + (n % 8 == 0 ? 3 : 0);
+  return cudaLaunchKernelEx(&cfg, kernels[which],
                             maps, a_scales, w_scales, a_gscale, w_gscale,
                             groups > 1 ? offs : (const int64_t*)nullptr, sh, out) == cudaSuccess
              ? TRACE_OK
