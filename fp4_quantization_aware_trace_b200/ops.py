@@ -4,7 +4,8 @@ Argument marshalling only: every step of the path runs in the library's
 CUDA kernels.  Tensors must be CUDA tensors; bf16 data is passed by pointer
 as raw 16-bit words.  Calls are asynchronous on the given stream (default:
 torch's current stream).  If the library is missing or fails to load, the
-first call raises -- there is no fallback of any kind.
+first call raises -- there is no fallback of any kind.  The expert operators
+make their usual call through csrc/binding.cpp, one native step.
 
 Method: rcap.io post "TRACE: Rollout-Guided Quantization-Aware Training for
 FP4" -- rollout capture of the compact cache (1 mantissa bit + scales), the
@@ -831,6 +832,14 @@ def _ptrs(*tensors):
     return [0 if t is None else t.data_ptr() for t in tensors]
 
 
+def _written(*outputs) -> None:
+    """Tells autograd of what the library has written into the caller's own
+    tensors: a backward pass that still needs what they held is then refused."""
+    for t in outputs:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _want(t: torch.Tensor, what: str, dtype, shape=None) -> None:
     if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise TraceError(f"{what}: unexpected dtype {t.dtype}")
@@ -870,7 +879,8 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, out: MoeRoute | None = 
     if nbytes == 0:
         raise TraceError(f"moe_sort: {num_experts} experts for [{tokens}, {k}] ids")
     with _On(stream, expert_ids, workspace) as s:
-        if out is None:
+        given = out is not None
+        if not given:
             new = lambda *shape: expert_ids.new_empty(shape, dtype=torch.int32)  # noqa: E731
             out = MoeRoute(expert_ids.new_empty(num_experts + 2, dtype=torch.int64), new(tokens, k),
                            new(tokens * k))
@@ -885,6 +895,8 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, out: MoeRoute | None = 
         st = lib.trace_moe_sort(ids, expert_ids.element_size(), tokens, k, num_experts, offsets, rows,
                                 slots, ws, workspace.numel() * workspace.element_size(), s)
         _check(st, "trace_moe_sort")
+        if given:
+            _written(out.offsets, out.rows, out.slots)
     return out
 
 
@@ -906,13 +918,16 @@ def moe_dispatch_fwd(x: torch.Tensor, route: MoeRoute, out: torch.Tensor | None 
     if rows != tokens:
         raise TraceError(f"{rows} tokens, and a route of {tokens}")
     with _On(stream, x, route.rows, route.slots, out) as s:
-        if out is None:
-            out = x.new_empty((tokens * k, cols))
-        else:
+        given = out is not None
+        if given:
             _want(out, "out", torch.bfloat16, (tokens * k, cols))
+        else:
+            out = x.new_empty((tokens * k, cols))
         px, rows, slots, po = _ptrs(x, route.rows, route.slots, out)
         _check(library().trace_moe_dispatch(px, tokens, k, cols, rows, slots, po, s),
                "trace_moe_dispatch")
+        if given:
+            _written(out)
     return out
 
 
@@ -932,13 +947,16 @@ def moe_combine_fwd(y: torch.Tensor, route: MoeRoute, weights: torch.Tensor | No
     if weights is not None:
         _want(weights, "weights", torch.float32, (tokens, k))
     with _On(stream, y, route.rows, weights, out) as s:
-        if out is None:
-            out = y.new_empty((tokens, cols))
-        else:
+        given = out is not None
+        if given:
             _want(out, "out", torch.bfloat16, (tokens, cols))
+        else:
+            out = y.new_empty((tokens, cols))
         py, rows, w, po = _ptrs(y, route.rows, weights, out)
         _check(library().trace_moe_combine(py, tokens, k, cols, rows, w, po, s),
                "trace_moe_combine")
+        if given:
+            _written(out)
     return out
 
 
@@ -1068,10 +1086,11 @@ def _matmul(a, w, cols, offsets, matrices, out, workspace, stream, bs):
     n = wrows // matrices
     ga, gw = (a.gscale, w.gscale) if bs == 16 else (None, None)
     with _On(stream, a.codes, a.scales, w.codes, w.scales, offsets, ga, gw, out, workspace) as s:
-        if out is None:
-            out = a.codes.new_empty((rows, n), dtype=torch.bfloat16)
-        else:
+        given = out is not None
+        if given:
             _want(out, "out", torch.bfloat16, (rows, n))
+        else:
+            out = a.codes.new_empty((rows, n), dtype=torch.bfloat16)
         if workspace is None:
             nbytes = trace_matmul_workspace_bytes(bs == 32, rows, cols, groups, la, n, matrices, lw)
             workspace = a.codes.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
@@ -1089,6 +1108,8 @@ def _matmul(a, w, cols, offsets, matrices, out, workspace, stream, bs):
             st = library().trace_mx_matmul_ws(ac, asc, rows, cols, groups, pf, la, wc, wsc, n,
                                               matrices, lw, po, pws, nbytes, s)
         _check(st, "trace_fp4_matmul" if bs == 16 else "trace_mx_matmul")
+        if given:
+            _written(out)
     return out
 
 

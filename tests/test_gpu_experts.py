@@ -851,3 +851,27 @@ def test_product_of_the_longest_rows(groups):
     assert ops.matmul_status()
     out = ops.fp4_matmul(a, ops.Capture(a.codes, None, a.scales, unit))
     assert ops.matmul_status() and out.flatten().tolist() == [2.0 ** 21] * groups
+
+
+def test_outputs_that_a_backward_pass_still_needs():
+    """A route or rows written anew between the two directions: refused, not wrong."""
+    tokens, k, cols = 12, 2, 64
+    g = _gen(9)
+    ids = torch.randint(0, 4, (tokens, k), generator=g).to(DEV)
+    x = torch.randn(tokens, cols, generator=g).bfloat16().to(DEV).requires_grad_()
+    w = torch.rand(tokens, k, generator=g).to(DEV).requires_grad_()
+    route = ops.moe_sort(ids, 4)
+    y = ops.moe_dispatch(x, route)
+    ops.moe_sort(ids.flip(0).contiguous(), 4, out=route)
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
+    rows = ops.moe_dispatch_fwd(x.detach(), route)
+    out = ops.moe_combine(rows, route, w)
+    ops.moe_dispatch_fwd(x.detach() * 2, route, out=rows)
+    with pytest.raises(RuntimeError):
+        out.sum().backward()
+    with torch.inference_mode():  # tensors without a version
+        again = ops.moe_sort(ids, 4)
+        ops.moe_sort(ids, 4, out=again)
+    ops.moe_combine(ops.moe_dispatch(x, route), route, w).sum().backward()
+    assert x.grad is not None and w.grad is not None
