@@ -77,7 +77,9 @@ __device__ __forceinline__ uint32_t same_key(uint32_t key, uint32_t bits) {
 // together: a warp's keys, and the counts of all chunks of five experts; and the
 // warps' counters of an expert are scanned by a warp, not by a thread (65536 x 8
 // slots, 128 experts: 12.8 us for both passes; 17.4 us with the counts of one
-// expert at a time and a thread for each expert's counters).
+// expert at a time and a thread for each expert's counters).  A sort by one CTA
+// takes a warp for every 64 slots or 32 experts (1 x 8 slots, 128 experts: 2.3 us,
+// with 32 warps 3.9).
 constexpr uint32_t kSortAtOnce = 5u;  // experts of a warp whose counts are read together
 template <typename ID>
 __global__ void __launch_bounds__(32 * kSortMaxWarps)
@@ -136,8 +138,8 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps)
       if (key[i] < n) atomicAdd(&mine[key[i]], 1u);
   }
   __syncthreads();
-  if (counts == nullptr) {  // this CTA's counts are all there are
-    for (uint32_t e = threadIdx.x; e < n; e += blockDim.x) earlier[e] = 0u;
+  const bool few = warps <= 8u;  // warps, whose counters of an expert a thread walks
+  if (counts == nullptr && !few) {  // this CTA's counts are all there are
     for (uint32_t e = warp; e < n; e += warps) {
       const uint32_t t = __reduce_add_sync(0xFFFFFFFFu, lane < warps ? next[lane * stride + e] : 0u);
       if (lane == 0) all[e] = t;
@@ -147,7 +149,14 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps)
   // exclusive scan of the totals over the CTA: earlier[e] becomes the chunk's
   // first row of expert e
   for (uint32_t e0 = 0; e0 < n; e0 += blockDim.x) {
-    const uint32_t e = e0 + threadIdx.x, total = e < n ? all[e] : 0u;
+    const uint32_t e = e0 + threadIdx.x;
+    uint32_t total = 0u;
+    if (e < n) {
+      if (counts != nullptr || !few)
+        total = all[e];
+      else
+        for (uint32_t w = 0; w < warps; ++w) total += next[w * stride + e];
+    }
     uint32_t sum = total;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -162,23 +171,32 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps)
     if (threadIdx.x == blockDim.x - 1u) carry = at + total;
     if (e < n) {
       if (blockIdx.x == 0) offsets[e] = (int64_t)at;
-      earlier[e] += at;
+      uint32_t row = counts != nullptr ? at + earlier[e] : at;
+      if (few)
+        for (uint32_t w = 0; w < warps; ++w) {
+          const uint32_t v = next[w * stride + e];
+          next[w * stride + e] = row;
+          row += v;
+        }
+      else
+        earlier[e] = row;
     }
     __syncthreads();
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) offsets[n] = (int64_t)slots;
-  // of each expert the warps' counters, a lane each
-  for (uint32_t e = warp; e < n; e += warps) {
-    const uint32_t v = lane < warps ? next[lane * stride + e] : 0u;
-    uint32_t sum = v;
+  if (!few) {  // of each expert the warps' counters, a lane each
+    for (uint32_t e = warp; e < n; e += warps) {
+      const uint32_t v = lane < warps ? next[lane * stride + e] : 0u;
+      uint32_t sum = v;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-      if (lane >= (uint32_t)d) sum += u;
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= (uint32_t)d) sum += u;
+      }
+      if (lane < warps) next[lane * stride + e] = earlier[e] + sum - v;
     }
-    if (lane < warps) next[lane * stride + e] = earlier[e] + sum - v;
+    __syncthreads();
   }
-  __syncthreads();
   const uint32_t bits = 32u - (uint32_t)__clz((int)n);
   for (uint32_t s0 = lo; s0 < hi; s0 += 128u) {
     if (!once) sort_keys(ids, s0, hi, E, n, key);

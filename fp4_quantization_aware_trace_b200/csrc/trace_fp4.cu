@@ -67,6 +67,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "trace_fp4.h"
 
 namespace {
@@ -288,6 +290,10 @@ int moe_sort_launch(const ID* ids, uint32_t slots, uint32_t E, int64_t* offsets,
     attr_set[dev] = true;
   }
   if (warps > (uint32_t)kSortMaxWarps) warps = kSortMaxWarps;
+  if (chunks <= 1) {  // few slots: few warps
+    const uint32_t want = std::max((slots + 63u) / 64u, (E + 32u) / 32u);
+    if (warps > want) warps = want;
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
