@@ -875,3 +875,13 @@ def test_outputs_that_a_backward_pass_still_needs():
         ops.moe_sort(ids, 4, out=again)
     ops.moe_combine(ops.moe_dispatch(x, route), route, w).sum().backward()
     assert x.grad is not None and w.grad is not None
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,n,cols,counts", [
+    (700, 1003, 96, [300, 1, 399]), (517, 390, 160, None), (518, 389, 2080, None),
+    (901, 1021, 64, [129, 501, 271]), (900, 262, 192, [127, 500, None]), (99, 95, 64, [33, 50, 16]),
+    (64, 33, 320, None), (150, 31, 320, None), (400, 2047, 64, None)])
+def test_product_rows_that_begin_anywhere(fmt, rows, n, cols, counts):
+    """Rows of out at odd elements: whole pieces as words, edges one by one."""
+    _product_case(rows, n, cols, fmt, True, True, counts, seed=rows * 3 + n)
