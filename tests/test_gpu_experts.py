@@ -885,3 +885,45 @@ def test_outputs_that_a_backward_pass_still_needs():
 def test_product_rows_that_begin_anywhere(fmt, rows, n, cols, counts):
     """Rows of out at odd elements: whole pieces as words, edges one by one."""
     _product_case(rows, n, cols, fmt, True, True, counts, seed=rows * 3 + n)
+
+
+def test_gradients_under_checkpoints_anomaly_checks_and_threads():
+    """Saved tensors packed and recomputed, traces kept of each node, calls from
+    several threads on streams of their own: the same gradients."""
+    import threading
+    from torch.utils.checkpoint import checkpoint
+    tokens, k, cols = 33, 3, 128
+    route, _ = _route(tokens, k, 5, 6)
+    g = _gen(12)
+    x = torch.randn(tokens, cols, generator=g).bfloat16().to(DEV).requires_grad_()
+    w = torch.rand(tokens, k, generator=g).to(DEV).requires_grad_()
+    do = torch.randn(tokens, cols, generator=g).bfloat16().to(DEV)
+
+    def layer(x, w):
+        return ops.moe_combine(ops.moe_dispatch(x, route) * 2, route, w)
+
+    want = torch.autograd.grad(layer(x, w), (x, w), do)
+    got = [torch.autograd.grad(checkpoint(layer, x, w, use_reentrant=False), (x, w), do)]
+    with torch.autograd.graph.save_on_cpu():
+        got.append(torch.autograd.grad(layer(x, w), (x, w), do))
+    with torch.autograd.detect_anomaly(check_nan=False):
+        got.append(torch.autograd.grad(layer(x, w), (x, w), do))
+
+    def work(to):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.default_stream())
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                out = torch.autograd.grad(layer(x, w), (x, w), do)
+        s.synchronize()
+        to.append(out)
+
+    threads = [threading.Thread(target=work, args=(got,)) for _ in range(4)]
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 7
+    for pair in got:
+        assert all(torch.equal(a, b) for a, b in zip(pair, want))
