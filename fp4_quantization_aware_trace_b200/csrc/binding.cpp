@@ -47,7 +47,12 @@ const at::Tensor* usual(PyObject* o, at::ScalarType type, int index) {
              : nullptr;
 }
 
-bool needs_grad(const at::Tensor& t) { return c10::GradMode::is_enabled() && t.requires_grad(); }
+// Whether a call has to go through the autograd function: to record it, or, with
+// a tangent of forward-mode differentiation (which no_grad leaves on), for that
+// function to refuse it.
+bool needs_grad(const at::Tensor& t) {
+  return (c10::GradMode::is_enabled() && t.requires_grad()) || t._fw_grad(/*level=*/0).defined();
+}
 
 void* at_of(const at::Tensor& t) { return t.data_ptr(); }
 

@@ -1017,13 +1017,12 @@ class MoeCombine(torch.autograd.Function):
 
 def moe_dispatch(x: torch.Tensor, route: MoeRoute) -> torch.Tensor:
     """Differentiable dispatch of tokens into expert order (for
-    capture(y, route.offsets) and the grouped product)."""
+    capture(y, route.offsets) and the grouped product).  Tensors that carry a
+    tangent of forward-mode differentiation are refused, here and in moe_combine."""
     y = (_bind or binding()).dispatch(x, route.rows, route.slots)
     if y is not None:
         return y
-    if torch.is_grad_enabled() and x.requires_grad:
-        return MoeDispatch.apply(x, route)
-    return moe_dispatch_fwd(x, route)
+    return MoeDispatch.apply(x, route)
 
 
 def moe_combine(y: torch.Tensor, route: MoeRoute, weights: torch.Tensor) -> torch.Tensor:
@@ -1031,9 +1030,9 @@ def moe_combine(y: torch.Tensor, route: MoeRoute, weights: torch.Tensor) -> torc
     out = (_bind or binding()).combine(y, route.rows, route.slots, weights)
     if out is not None:
         return out
-    if torch.is_grad_enabled() and (y.requires_grad or weights.requires_grad):
-        return MoeCombine.apply(y, route, weights)
-    return moe_combine_fwd(y, route, weights)
+    if weights is None:
+        raise TraceError("moe_combine needs weights (moe_combine_fwd takes None for all ones)")
+    return MoeCombine.apply(y, route, weights)
 
 
 def _matmul_operand(cap, cols: int, bs: int, what: str) -> tuple[int, int]:
