@@ -38,7 +38,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     library's path."""
     build_binding(force)
     deps = [HDR] + [os.path.join(CSRC_DIR, f) for f in os.listdir(CSRC_DIR)
-                    if f.endswith((".cu", ".cuh"))]
+                    if f.endswith((".cu", ".cuh", ".h"))]
     if (not force and os.path.exists(LIB)
             and os.path.getmtime(LIB) >= max(os.path.getmtime(d) for d in deps)):
         return LIB

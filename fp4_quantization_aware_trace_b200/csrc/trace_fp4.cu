@@ -69,6 +69,7 @@
 
 #include <algorithm>
 
+#include "plan.h"
 #include "trace_fp4.h"
 
 namespace {
@@ -496,10 +497,9 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
       ? (long double)((rows + sh.nt - 1) / sh.nt) * sh.n_tiles
       : ((long double)rows / sh.nt + 2.0L * groups) * (long double)sh.n_tiles;
   if (tiles >= 2147483648.0L) return TRACE_ERR_SHAPE;
-  sh.split = 1;
-  if (groups == 1 && !pair)
-    while (sh.split < kMmMaxSplit && tiles * (sh.split * 2) <= 128 && sh.ksteps >= sh.split * 2)
-      sh.split *= 2;
+  sh.split = groups == 1 && !pair
+                 ? matmul_split((uint64_t)tiles, sh.ksteps, (uint32_t)sms, kMmMaxSplit)
+                 : 1;
   MmMaps maps;
   int st = code_map(&maps.a, a_codes, (uint64_t)rows, (uint64_t)cols / 2,
                     pair ? kMmPairBox : sh.nt);
