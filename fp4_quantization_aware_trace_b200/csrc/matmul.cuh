@@ -405,7 +405,8 @@ struct MmTile {
   bool end;           // behind the last tile
 };
 
-// Offsets are clamped to the rows there are, whatever they hold.
+// Offsets are clamped to the rows there are, whatever they hold.  One group may
+// have some too: a batch padded around it.
 __device__ __forceinline__ int64_t mm_bound(const int64_t* offs, int32_t g, const MmShape& sh) {
   if (offs == nullptr) return g == 0 ? 0 : sh.rows;
   const int64_t v = offs[g];
@@ -589,7 +590,7 @@ __device__ __forceinline__ void copy_scales(const ScaleSrc& s, const uint8_t* ba
 // the same tokens: each CTA copies its own 128 rows of w, half of the tokens'
 // codes and all of their scales, every part by TMA and counted on the leader's
 // barrier, and the leader's warp 1 issues for both.
-//   TR (pairs, one group, rows of out in whole 16 bytes): called with the operands
+//   TR (pairs, one group without offsets, rows of out in whole 16 bytes): called with the operands
 // exchanged, so the "tokens" of these comments are columns of out and the rows
 // of w its rows.  A lane then holds 16 columns of a row and not 16 rows of a
 // column, nothing has to be turned, and a warp hands 32 x 32 of them to the copy

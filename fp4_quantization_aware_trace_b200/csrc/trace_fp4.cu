@@ -466,8 +466,9 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
     if (plan.retile_a) a_scales = a.dst;
     if (plan.retile_w) w_scales = w.dst;
   }
-  // out transposed, see k_matmul: (scales are all tiled by now)
-  const bool tr = pair && groups == 1 && n % 8 == 0;
+  // out transposed, see k_matmul: (scales are all tiled by now; not with bounds,
+  // which the copy engine's boxes of out cannot keep to)
+  const bool tr = pair && groups == 1 && offs == nullptr && n % 8 == 0;
   if (tr) {
     exchange(&a_codes, &w_codes);
     exchange(&a_scales, &w_scales);
@@ -546,8 +547,8 @@ int matmul_launch(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   cfg.numAttrs = 2;
   const int which = tr ? 6 : (pair ? 2 : rb == 1 ? 0 : 1) + (n % 8 == 0 ? 3 : 0);
   return cudaLaunchKernelEx(&cfg, kernels[which],
-                            maps, a_scales, w_scales, a_gscale, w_gscale,
-                            groups > 1 ? offs : (const int64_t*)nullptr, sh, out) == cudaSuccess
+                            maps, a_scales, w_scales, a_gscale, w_gscale, offs, sh,
+                            out) == cudaSuccess
              ? TRACE_OK
              : TRACE_ERR_CUDA;
 }

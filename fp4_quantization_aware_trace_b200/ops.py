@@ -1117,7 +1117,8 @@ def fp4_matmul(a: Capture, w: Capture, cols: int | None = None, out: torch.Tenso
     """Product of two NVFP4 captures, bf16 [rows, n]: a of [rows, cols], w of
     one matrix [n, cols], or of one per expert stacked by rows (w.gscale has
     one entry per matrix, a.offsets groups the rows).  Rows of a's groups
-    behind w's matrices (dropped slots) become zero.  cols is needed when
+    behind w's matrices (dropped slots) become zero; rows outside a.offsets
+    are left as they were in `out` (undefined if None).  cols is needed when
     both scales are tiled.  Large products copy scales that are not tiled
     into `workspace` (trace_matmul_workspace_bytes; allocated if None).  Has
     no gradient: codes are the rollout's; the

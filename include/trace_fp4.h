@@ -537,7 +537,8 @@ int trace_moe_combine_bwd(const uint16_t* grad_out, const uint16_t* y, int64_t t
  *             w_gscale float[num_matrices].  num_matrices <= num_groups <=
  *             TRACE_MATMUL_MAX_GROUPS; rows of the groups from num_matrices
  *             on (the dropped slots of trace_moe_sort) become +0, and rows
- *             from offsets[num_groups] on are left as they were.
+ *             in front of offsets[0] and from offsets[num_groups] on are left
+ *             as they were (of one group too).
  *   layouts : TRACE_SCALES_*, one for each operand.  The padding of a tiled
  *             array is not used, whatever it holds.
  *   out     : bf16 [rows, n], 16-byte aligned; must not overlap an input.

@@ -61,3 +61,44 @@ def test_forward_mode_is_refused(way, grad):
                 call()
         assert torch.equal(ops.moe_dispatch(x, route), y)
         assert fwd.unpack_dual(ops.moe_combine(y, route, w)).tangent is None
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tiled", [False, True])
+@pytest.mark.parametrize("rows,n,cols,lo,hi", [
+    (70, 96, 128, 0, 41), (70, 96, 128, 13, 41), (9, 2048, 2048, 2, 5), (900, 256, 128, 101, 700),
+    (900, 520, 512, 0, 513), (400, 250, 192, 399, 400), (700, 384, 256, 64, 64), (300, 129, 96, 128, 300),
+    (3000, 1000, 256, 130, 2900)])
+def test_one_group_with_bounds(way, fmt, tiled, rows, n, cols, lo, hi):
+    """A batch that is padded around its one group: the rows in front of
+    offsets[0] and from offsets[1] on are left as they were, in every form of the
+    product (single CTAs, k split, pairs, pairs that would write out transposed)."""
+    a = inputs.tiny_site(1, rows, cols).x_roll.to(DEV)
+    w = inputs.tiny_site(2, n, cols).x_roll.to(DEV)
+    offs = torch.tensor([lo, hi], dtype=torch.int64, device=DEV)
+    out = torch.full((rows, n), 5.0, dtype=torch.bfloat16, device=DEV)
+    if fmt == "nvfp4":
+        cap = ops.capture_tiled if tiled else ops.capture
+        ca, cw = cap(a), cap(w)
+        whole = ops.fp4_matmul(ca, cw, cols)
+        ca.offsets = offs
+        ops.fp4_matmul(ca, cw, cols, out=out)
+        fresh = ops.fp4_matmul(ca, cw, cols)
+    else:
+        cap = ops.mx_capture_tiled if tiled else ops.mx_capture
+        ca, cw = cap(a), cap(w)
+        whole = ops.mx_matmul(ca, cw, cols)
+        ops.mx_matmul(ca, cw, cols, offsets=offs, out=out)
+        fresh = ops.mx_matmul(ca, cw, cols, offsets=offs)
+    s, scols = (ca.scales, cw.scales), cols // (16 if fmt == "nvfp4" else 32)
+    sa, sw = (v.cpu().numpy() if v.dim() == 2 else ref.untile(v.cpu().numpy(), r, scols)
+              for v, r in zip(s, (rows, n)))
+    ga, gw = (ca.gscale.cpu().numpy(), cw.gscale.cpu().numpy()) if fmt == "nvfp4" else (None, None)
+    exact, mag = ref.product(ref.operand(ca.codes.cpu().numpy(), sa, rows, cols, fmt),
+                             ref.operand(cw.codes.cpu().numpy(), sw, n, cols, fmt), ga, gw, [0, rows], n)
+    bound = ref.product_bound(exact, mag, cols)
+    for got in (out, fresh):
+        assert np.all(np.abs(ref.f64(got) - exact)[lo:hi] <= bound[lo:hi])
+    assert np.all(np.abs(ref.f64(whole) - exact) <= bound)
+    assert bool((out[:lo] == 5.0).all()) and bool((out[hi:] == 5.0).all())
+    assert ops.matmul_status()
