@@ -115,15 +115,19 @@ PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
-// Rows of an operand's codes and its scales' layout; false if they do not fit.
+// Rows of an operand's codes and its scales' layout; false if they do not fit:
+// [rows, cols / block] row-major, or flat in the tiled layout.
 bool operand(const at::Tensor& codes, const at::Tensor& scales, int64_t cols, int64_t block,
              int64_t* rows, int* layout) {
   *rows = codes.numel() * 2 / cols;
   if (*rows * cols != codes.numel() * 2) return false;
   const int64_t c = cols / block;
-  const bool plain = scales.dim() == 2;
-  *layout = plain ? TRACE_SCALES_ROW_MAJOR : TRACE_SCALES_TILED_128x4;
-  return scales.numel() == (plain ? *rows * c : (*rows + 127) / 128 * ((c + 3) / 4) * 512);
+  if (scales.dim() == 2) {
+    *layout = TRACE_SCALES_ROW_MAJOR;
+    return scales.size(0) == *rows && scales.size(1) == c;
+  }
+  *layout = TRACE_SCALES_TILED_128x4;
+  return scales.dim() == 1 && scales.numel() == (*rows + 127) / 128 * ((c + 3) / 4) * 512;
 }
 
 // matmul(block, cols, matrices, offsets, a_codes, a_scales, a_gscale, w_codes, w_scales, w_gscale)

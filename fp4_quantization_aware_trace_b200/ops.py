@@ -1046,11 +1046,12 @@ def _matmul_operand(cap, cols: int, bs: int, what: str) -> tuple[int, int]:
         raise TraceError(f"{what}: {codes.numel()} bytes of codes are no rows of {cols}")
     c = cols // bs
     if scales.dim() == 2:
-        layout, want = TRACE_SCALES_ROW_MAJOR, rows * c
+        layout, want = TRACE_SCALES_ROW_MAJOR, (rows, c)
     else:
-        layout, want = TRACE_SCALES_TILED_128x4, -(-rows // 128) * -(-c // 4) * 512
-    if scales.numel() != want:
-        raise TraceError(f"{what}: {scales.numel()} scales for [{rows}, {cols}]")
+        layout, want = TRACE_SCALES_TILED_128x4, (-(-rows // 128) * -(-c // 4) * 512,)
+    if scales.shape != want:
+        raise TraceError(f"{what}: scales of {tuple(scales.shape)} for [{rows}, {cols}], "
+                         f"expected {want}")
     return rows, layout
 
 

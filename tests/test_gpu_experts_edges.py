@@ -102,3 +102,27 @@ def test_one_group_with_bounds(way, fmt, tiled, rows, n, cols, lo, hi):
     assert np.all(np.abs(ref.f64(whole) - exact) <= bound)
     assert bool((out[:lo] == 5.0).all()) and bool((out[hi:] == 5.0).all())
     assert ops.matmul_status()
+
+
+def test_operands_of_other_lengths_are_refused(way):
+    """Rows of another length, whose bytes would make other rows of this one."""
+    x, w = (torch.randn(r, c, generator=_gen(r)).bfloat16().to(DEV) for r, c in ((64, 128), (40, 256)))
+    a, b = ops.capture(x), ops.capture(w)
+    ma, mb = ops.mx_capture(x), ops.mx_capture(w)
+    for call in (lambda **k: ops.fp4_matmul(a, b, **k), lambda **k: ops.fp4_matmul(b, a, **k),
+                 lambda **k: ops.fp4_matmul(b, b, 128, **k), lambda **k: ops.mx_matmul(ma, mb, **k),
+                 lambda **k: ops.mx_matmul(mb, mb, 512, **k)):
+        for kw in ({}, {"stream": torch.cuda.current_stream()}):
+            with pytest.raises(ops.TraceError):
+                call(**kw)
+    # one matrix per expert kept as [experts, n, cols / 16]: neither rows nor tiled
+    s = b.scales
+    e = ops.capture(torch.randn(4 * 64, 64, generator=_gen(1)).bfloat16().to(DEV),
+                    torch.arange(5, device=DEV) * 64)
+    e.scales = e.scales.view(4, 64, 4)
+    t = ops.capture(torch.randn(16, 64, generator=_gen(2)).bfloat16().to(DEV),
+                    torch.tensor([0, 4, 8, 12, 16], device=DEV))
+    for kw in ({}, {"stream": torch.cuda.current_stream()}):
+        with pytest.raises(ops.TraceError):
+            ops.fp4_matmul(t, e, 64, **kw)
+    assert s.dim() == 2 and ops.fp4_matmul(b, b).shape == (40, 40)
