@@ -84,7 +84,7 @@ struct MmShape {
 
 __device__ uint32_t g_matmul_gave_up;  // set if a wait ran out of polls
 
-// The product of two global scales as m * p * q, m in [1, 2) and p, q powers
+// The product of two global scales as m * p * q, |m| in [1, 2) and p, q powers
 // of two: ga * gw itself may leave fp32's range where sum * ga * gw does not
 // (a small activation against a large weight).  |sum| is 0 or in
 // [2^-20, 2^54], so with the exponents halved no step over- or underflows
@@ -121,7 +121,7 @@ __device__ __forceinline__ OutScale make_out_scale(float ga, float gw) {
   int e = ((__double2hiint(d) >> 20) & 0x7FF) - 1023;
   if (e == -1023 || e == 1024 || (e >= -60 && e <= 60)) return s;  // zero or not finite, or plain
   s.one = false;
-  s.m = (float)__hiloint2double((__double2hiint(d) & 0x000FFFFF) | (1023 << 20), __double2loint(d));
+  s.m = (float)__hiloint2double((__double2hiint(d) & 0x800FFFFF) | (1023 << 20), __double2loint(d));
   e = max(-252, min(e, 250));
   s.p = __int_as_float((e / 2 + 127) << 23);
   s.q = __int_as_float((e - e / 2 + 127) << 23);

@@ -126,3 +126,23 @@ def test_operands_of_other_lengths_are_refused(way):
         with pytest.raises(ops.TraceError):
             ops.fp4_matmul(t, e, 64, **kw)
     assert s.dim() == 2 and ops.fp4_matmul(b, b).shape == (40, 40)
+
+
+@pytest.mark.parametrize("ga,gw", [(-1e-38, 1e30), (3e35, -1e-36), (-1e30, 1e30), (-3.0, 2.0),
+                                   (-1e-25, -1e-10), (1e-25, -1e-10), (2.0 ** -140, -(2.0 ** 100))])
+def test_signs_of_global_scales(way, ga, gw):
+    """A caller's negative global scale turns the sign at every magnitude."""
+    rows, n, cols = 20, 24, 64
+    g = _gen(3)
+    codes = lambda r: torch.randint(0, 256, (r * cols // 2,), generator=g, dtype=torch.uint8)  # noqa: E731
+    s = torch.randint(0x20, 0x50, (rows + n, cols // 16), generator=g, dtype=torch.uint8)
+    a = ops.Capture(codes(rows).to(DEV), None, s[:rows].to(DEV), torch.tensor([ga], device=DEV))
+    w = ops.Capture(codes(n).to(DEV), None, s[rows:].to(DEV), torch.tensor([gw], device=DEV))
+    out = ref.f64(ops.fp4_matmul(a, w))
+    wide = ref.operand(a.codes.cpu().numpy(), s[:rows].numpy(), rows, cols, "nvfp4")
+    tall = ref.operand(w.codes.cpu().numpy(), s[rows:].numpy(), n, cols, "nvfp4")
+    exact, mag = ref.product(wide, tall, a.gscale.cpu().numpy(), w.gscale.cpu().numpy(), [0, rows], n)
+    over, inside = np.abs(exact) > 3.4e38, np.abs(exact) < 3.3e38
+    bound = ref.product_bound(exact, np.abs(mag), cols)
+    assert np.all(out[over] == np.sign(exact[over]) * np.inf)
+    assert np.all(np.abs(out - exact)[inside] <= bound[inside])
