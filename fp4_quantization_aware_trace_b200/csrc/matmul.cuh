@@ -82,7 +82,7 @@ struct MmShape {
   uint8_t a_bytes, w_bytes;    // row-major scales that are not 4-byte words
 };
 
-__device__ uint32_t g_matmul_gave_up;  // set if a wait ran out of polls
+__device__ uint32_t g_matmul_gave_up;  // counts waits that ran out of polls; never cleared
 
 // The product of two global scales as m * p * q, |m| in [1, 2) and p, q powers
 // of two: ga * gw itself may leave fp32's range where sum * ga * gw does not
@@ -217,7 +217,7 @@ __device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, volatile 
     if (__any_sync(0xFFFFFFFFu, *gave_up != 0u)) break;
   }
   *gave_up = 1u;
-  g_matmul_gave_up = 1u;
+  if (threadIdx.x % 32u == 0u) atomicAdd(&g_matmul_gave_up, 1u);
   return false;
 }
 

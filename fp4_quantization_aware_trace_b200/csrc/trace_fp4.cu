@@ -1310,19 +1310,16 @@ size_t trace_mx_matmul_workspace_bytes(int64_t rows, int64_t cols, int32_t num_g
 }
 
 int trace_matmul_status(void* stream) {
-  if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return TRACE_ERR_CUDA;
-  uint32_t word = 0;
-  if (cudaMemcpyFromSymbolAsync(&word, g_matmul_gave_up, 4, 0, cudaMemcpyDeviceToHost,
+  static thread_local Told told;
+  int dev = 0;
+  uint32_t count = 0;
+  if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess ||
+      cudaGetDevice(&dev) != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&count, g_matmul_gave_up, 4, 0, cudaMemcpyDeviceToHost,
                                 (cudaStream_t)stream) != cudaSuccess ||
       cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess)
     return TRACE_ERR_CUDA;
-  if (word == 0) return TRACE_OK;
-  const uint32_t zero = 0;
-  if (cudaMemcpyToSymbolAsync(g_matmul_gave_up, &zero, 4, 0, cudaMemcpyHostToDevice,
-                              (cudaStream_t)stream) != cudaSuccess ||
-      cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess)
-    return TRACE_ERR_CUDA;
-  return TRACE_ERR_TIMEOUT;
+  return told.news(dev, stream, count) ? TRACE_ERR_TIMEOUT : TRACE_OK;
 }
 
 int trace_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows, int64_t cols,

@@ -1142,7 +1142,8 @@ def mx_matmul(a: MxCapture, w: MxCapture, cols: int | None = None,
 
 def matmul_status(stream=None) -> bool:
     """True when no product on the current device has given up a wait since
-    the last check (trace_matmul_status: waits for the stream)."""
+    this thread last asked about this stream (trace_matmul_status: waits for
+    the stream)."""
     st = library().trace_matmul_status(_stream(stream))
     if st == TRACE_ERR_TIMEOUT:
         return False

@@ -38,11 +38,12 @@
  *
  * Ownership and execution: every pointer except `stream` is a DEVICE
  * pointer owned by the caller; the library never allocates, frees or
- * synchronises.  All calls are asynchronous on `stream` (a cudaStream_t
- * passed as void*, NULL = the legacy default stream).  The library holds no
- * mutable global state apart from a per-device cache of the SM count (and
- * the static scratch of trace_capture_static_ws, see there), so it may be
- * called from several host threads.  Every call that takes its scratch
+ * synchronises (but for the two status calls).  All calls are asynchronous on
+ * `stream` (a cudaStream_t passed as void*, NULL = the legacy default stream).
+ * The library holds no mutable global state apart from per-device caches (the
+ * SM count, kernel attributes), the static scratch of trace_capture_static_ws
+ * and the counter of trace_matmul_status (see there), so it may be called from
+ * several host threads.  Every call that takes its scratch
  * memory from the caller is capturable into a CUDA graph.
  *
  * Contents, in order: status and version; workspace and record-size queries;
@@ -583,11 +584,14 @@ int trace_mx_matmul_ws(const uint8_t* a_codes, const uint8_t* a_scales, int64_t 
                        void* workspace, size_t workspace_bytes, void* stream);
 
 /* Whether a product on the current device has given up a wait for its own
- * copies since the last check (every wait is bounded; none is expected to
- * run out): waits for the work queued on `stream`, reads and clears one word
- * of the library per GPU and returns TRACE_ERR_TIMEOUT if it was set (the
- * outputs since the last check are then not valid), else TRACE_OK.  Not for
- * use during stream capture (it synchronises). */
+ * copies (every wait is bounded; none is expected to run out): waits for the
+ * work queued on `stream`, reads a counter that the library keeps per GPU and
+ * never clears, and returns TRACE_ERR_TIMEOUT if it has grown since the calling
+ * thread last asked about this stream (the first time: at all), else TRACE_OK.
+ * After TRACE_ERR_TIMEOUT the outputs of this stream since then are not to be
+ * trusted; the counter is one for all streams, so a failure on another stream
+ * is told here too.  Nobody's question hides the answer from another thread or
+ * stream.  Not for use during stream capture (it synchronises). */
 int trace_matmul_status(void* stream);
 
 #ifdef __cplusplus

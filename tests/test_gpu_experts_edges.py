@@ -146,3 +146,26 @@ def test_signs_of_global_scales(way, ga, gw):
     bound = ref.product_bound(exact, np.abs(mag), cols)
     assert np.all(out[over] == np.sign(exact[over]) * np.inf)
     assert np.all(np.abs(out - exact)[inside] <= bound[inside])
+
+
+def test_status_of_products_from_several_threads():
+    """Each thread and stream asks for itself, while products run on both."""
+    import threading
+    a = ops.capture_tiled(inputs.tiny_site(1, 300, 512).x_roll.to(DEV))
+    w = ops.capture_tiled(inputs.tiny_site(2, 384, 512).x_roll.to(DEV))
+    said = []
+
+    def work():
+        s = torch.cuda.Stream()
+        for _ in range(50):
+            ops.fp4_matmul(a, w, 512, stream=s)
+            said.append(ops.matmul_status(s))
+        said.append(ops.matmul_status())
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(said) == 4 * 51 and all(said)
