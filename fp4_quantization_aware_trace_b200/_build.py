@@ -33,10 +33,20 @@ def nvcc() -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile the library, and the Python module beside it where torch, the
+    Python headers and g++ are there; returns the library's path.  A caller from
+    C needs nothing but nvcc: without the module only ops.binding() fails."""
+    build_library(force, verbose)
+    try:
+        build_binding(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        sys.stderr.write(f"{os.path.basename(BIND)} has not been built: {e}\n")
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/trace_fp4.cu (which includes the csrc/*.cuh kernels) into
-    the package directory, and the Python module beside it; returns the
-    library's path."""
-    build_binding(force)
+    the package directory; returns the library's path."""
     deps = [HDR] + [os.path.join(CSRC_DIR, f) for f in os.listdir(CSRC_DIR)
                     if f.endswith((".cu", ".cuh", ".h"))]
     if (not force and os.path.exists(LIB)
@@ -61,6 +71,8 @@ def build_binding(force: bool = False) -> str:
     if (not force and os.path.exists(BIND)
             and os.path.getmtime(BIND) >= max(os.path.getmtime(d) for d in (HDR, BIND_SRC))):
         return BIND
+    if os.path.exists(BIND):  # outdated: not to be loaded if this fails
+        os.unlink(BIND)
     import sysconfig
 
     import torch

@@ -1,8 +1,11 @@
 """The FP4 expert operators' host side off the usual path (no GPU)."""
 from __future__ import annotations
 
+import importlib.util
 import os
+import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -42,3 +45,50 @@ def test_operands_of_other_lengths_are_refused():
     ma, mw = ops.MxCapture(u8(4 * 64), None, u8(4, 4)), ops.MxCapture(u8(6 * 128), None, u8(6, 8))
     with pytest.raises(ops.TraceError, match="scales of"):
         ops.mx_matmul(ma, mw)
+
+
+def _tree(tmp_path, monkeypatch):
+    """A copy of the build files whose compilers only write their outputs: the
+    module _build of it, and the commands that it has run."""
+    root = tmp_path / "tree"
+    shutil.copytree(CSRC, root / "pkg" / "csrc")
+    shutil.copytree(os.path.join(os.path.dirname(HERE), "include"), root / "include")
+    shutil.copy(os.path.join(os.path.dirname(CSRC), "_build.py"), root / "pkg")
+    spec = importlib.util.spec_from_file_location("_build_of_a_copy", root / "pkg" / "_build.py")
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(os.path.basename(cmd[0]))
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("built")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(mod.subprocess, "run", run)
+    return mod, ran
+
+
+def _modules(mod):
+    return sorted(f for f in os.listdir(mod.PKG) if f.startswith("_binding"))
+
+
+@pytest.mark.parametrize("missing", ["torch", "g++", "headers"])
+def test_the_library_is_built_without_the_module(tmp_path, monkeypatch, missing):
+    mod, ran = _tree(tmp_path, monkeypatch)
+    if missing == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)  # import torch raises ImportError
+    run = mod.subprocess.run
+
+    def some(cmd, **kw):
+        if os.path.basename(cmd[0]) == "g++" and missing == "g++":
+            raise FileNotFoundError("g++")
+        r = run(cmd, **kw)
+        if os.path.basename(cmd[0]) == "g++" and missing == "headers":
+            r.returncode = 1
+        return r
+
+    monkeypatch.setattr(mod.subprocess, "run", some)
+    assert mod.build(force=True) == mod.LIB and os.path.exists(mod.LIB)
+    assert ran[0] == "nvcc" and not [f for f in _modules(mod) if f.endswith(".so")]
+    assert mod.build() == mod.LIB and ran.count("nvcc") == 1
