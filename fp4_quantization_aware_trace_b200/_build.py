@@ -3,15 +3,16 @@ the Python module beside it that calls it for torch tensors (g++)."""
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "trace_fp4.cu")
 CSRC_DIR = os.path.join(PKG, "csrc")
 BIND_SRC = os.path.join(PKG, "csrc", "binding.cpp")
-BIND = os.path.join(PKG, "_binding.so")
 HDR = os.path.join(ROOT, "include", "trace_fp4.h")
 LIB = os.path.join(PKG, "libtrace_fp4.so")
 
@@ -40,7 +41,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     try:
         build_binding(force)
     except (ImportError, OSError, RuntimeError) as e:
-        sys.stderr.write(f"{os.path.basename(BIND)} has not been built: {e}\n")
+        sys.stderr.write(f"the Python module of csrc/binding.cpp has not been built: {e}\n")
     return LIB
 
 
@@ -66,19 +67,27 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def binding_path() -> str:
+    """The module for this Python and the installed torch, whose C++ classes it is
+    compiled against: one built for others has another name and is not loaded."""
+    import torch
+    git = getattr(torch.version, "git_version", None) or ""
+    torch_id = re.sub(r"[^0-9A-Za-z.]", "_", f"{torch.__version__}-{git[:8]}")
+    return os.path.join(PKG, f"_binding.torch{torch_id}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_binding(force: bool = False) -> str:
     """Compile csrc/binding.cpp against the installed torch; returns the path."""
-    if (not force and os.path.exists(BIND)
-            and os.path.getmtime(BIND) >= max(os.path.getmtime(d) for d in (HDR, BIND_SRC))):
-        return BIND
-    if os.path.exists(BIND):  # outdated: not to be loaded if this fails
-        os.unlink(BIND)
-    import sysconfig
-
     import torch
+    path = binding_path()
+    if (not force and os.path.exists(path)
+            and os.path.getmtime(path) >= max(os.path.getmtime(d) for d in (HDR, BIND_SRC))):
+        return path
+    if os.path.exists(path):  # outdated: not to be loaded if this fails
+        os.unlink(path)
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
-    tmp = BIND + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_path("include"),
@@ -90,11 +99,10 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("g++ failed building _binding.so")
-    os.replace(tmp, BIND)
-    return BIND
+        raise RuntimeError("g++ failed")
+    os.replace(tmp, path)
+    return path
 
 
 if __name__ == "__main__":
-    build(force=True, verbose="-v" in sys.argv)
-    print(LIB, BIND)
+    print(build(force=True, verbose="-v" in sys.argv))

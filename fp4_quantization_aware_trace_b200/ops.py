@@ -17,10 +17,13 @@ import contextlib
 import ctypes
 import dataclasses
 import functools
+import importlib.util
 import os
 import threading
 
 import torch
+
+from . import _build
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtrace_fp4.so")
@@ -773,19 +776,23 @@ _bind = None
 def binding():
     """The module that makes the usual call of an expert operator in one native
     step (csrc/binding.cpp); each of its functions returns None for any other
-    call.  Raises if it has not been built."""
+    call.  Raises if it has not been built for this torch and Python."""
     global _bind
     if _bind is None:
         lib = library()
         with _lock:
-            if not os.path.exists(os.path.join(_PKG, "_binding.so")):
-                raise TraceError(f"{_PKG}/_binding.so is missing: it has not been built")
-            from . import _binding
-            _binding.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            path = _build.binding_path()
+            if not os.path.exists(path):
+                raise TraceError(f"{path} is missing: it has not been built for this torch")
+            name = f"{__package__}._binding"
+            spec = importlib.util.spec_from_file_location(name, path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 lib.trace_moe_sort, lib.trace_moe_sort_workspace_bytes, lib.trace_moe_dispatch,
                 lib.trace_moe_combine, lib.trace_moe_combine_bwd, lib.trace_fp4_matmul,
                 lib.trace_mx_matmul, lib.trace_fp4_matmul_workspace_bytes, lib.trace_mx_matmul_workspace_bytes)))
-            _bind = _binding
+            _bind = module
     return _bind
 
 

@@ -92,3 +92,21 @@ def test_the_library_is_built_without_the_module(tmp_path, monkeypatch, missing)
     assert mod.build(force=True) == mod.LIB and os.path.exists(mod.LIB)
     assert ran[0] == "nvcc" and not [f for f in _modules(mod) if f.endswith(".so")]
     assert mod.build() == mod.LIB and ran.count("nvcc") == 1
+
+
+def test_the_module_belongs_to_its_torch(tmp_path, monkeypatch):
+    """Built again for another torch or Python, and never loaded by them."""
+    mod, ran = _tree(tmp_path, monkeypatch)
+    first = mod.build_binding()
+    assert mod.build_binding() == first and ran == ["g++"]
+    monkeypatch.setattr(torch, "__version__", "99.0.1+cu999")
+    second = mod.build_binding()
+    assert second != first and ran == ["g++", "g++"]
+    monkeypatch.setattr(torch.version, "git_version", "0123456789abcdef")
+    third = mod.build_binding()
+    monkeypatch.setattr(mod.sysconfig, "get_config_var", lambda name: ".cpython-399-test.so")
+    assert len({first, second, third, mod.build_binding()}) == 4 and len(_modules(mod)) == 4
+    # the real one: only under the installed torch's name
+    monkeypatch.setattr(ops, "_bind", None)
+    with pytest.raises(ops.TraceError, match="has not been built"):
+        ops.binding()
