@@ -5,7 +5,8 @@ CUDA kernels.  Tensors must be CUDA tensors; bf16 data is passed by pointer
 as raw 16-bit words.  Calls are asynchronous on the given stream (default:
 torch's current stream).  If the library is missing or fails to load, the
 first call raises -- there is no fallback of any kind.  The expert operators
-make their usual call through csrc/binding.cpp, one native step.
+make their usual call through csrc/binding.cpp, one native step; where that
+module is missing they warn and make it from here, to the same kernels.
 
 Method: rcap.io post "TRACE: Rollout-Guided Quantization-Aware Training for
 FP4" -- rollout capture of the compact cache (1 mantissa bit + scales), the
@@ -20,6 +21,7 @@ import functools
 import importlib.util
 import os
 import threading
+import warnings
 
 import torch
 
@@ -778,7 +780,7 @@ def binding():
     step (csrc/binding.cpp); each of its functions returns None for any other
     call.  Raises if it has not been built for this torch and Python."""
     global _bind
-    if _bind is None:
+    if _bind is None or _bind is _NoBinding:
         lib = library()
         with _lock:
             path = _build.binding_path()
@@ -794,6 +796,30 @@ def binding():
                 lib.trace_mx_matmul, lib.trace_fp4_matmul_workspace_bytes, lib.trace_mx_matmul_workspace_bytes)))
             _bind = module
     return _bind
+
+
+class _NoBinding:
+    """Answers None to every call, as the module does to an unusual one: without
+    it ops.py goes its own way to the same kernels, which takes the host longer."""
+
+    @staticmethod
+    def matmul(*args):
+        return None
+
+    sort = dispatch = combine = matmul
+
+
+def _native():
+    """The module, or, with a warning, what stands in for it on a machine where it
+    has not been built (no g++ or Python headers) or does not load."""
+    global _bind
+    try:
+        return binding()
+    except (TraceError, ImportError, OSError) as e:
+        library()  # without the library there is no other way
+        warnings.warn(f"expert operators take longer to call: {e}", RuntimeWarning, stacklevel=3)
+        _bind = _NoBinding
+        return _bind
 
 
 class _On:
@@ -874,7 +900,7 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, out: MoeRoute | None = 
     """Stable sort of the slots of expert_ids (int32 / int64 [tokens, k]) by
     expert; ids outside [0, num_experts) drop their slot."""
     if out is None and workspace is None and stream is None:
-        got = (_bind or binding()).sort(expert_ids, num_experts)
+        got = (_bind or _native()).sort(expert_ids, num_experts)
         if got is not None:
             return MoeRoute(*got)
     if expert_ids.dim() != 2 or expert_ids.shape[1] < 1:
@@ -1026,7 +1052,7 @@ def moe_dispatch(x: torch.Tensor, route: MoeRoute) -> torch.Tensor:
     """Differentiable dispatch of tokens into expert order (for
     capture(y, route.offsets) and the grouped product).  Tensors that carry a
     tangent of forward-mode differentiation are refused, here and in moe_combine."""
-    y = (_bind or binding()).dispatch(x, route.rows, route.slots)
+    y = (_bind or _native()).dispatch(x, route.rows, route.slots)
     if y is not None:
         return y
     return MoeDispatch.apply(x, route)
@@ -1034,7 +1060,7 @@ def moe_dispatch(x: torch.Tensor, route: MoeRoute) -> torch.Tensor:
 
 def moe_combine(y: torch.Tensor, route: MoeRoute, weights: torch.Tensor) -> torch.Tensor:
     """Differentiable return to token order, weighted by the router."""
-    out = (_bind or binding()).combine(y, route.rows, route.slots, weights)
+    out = (_bind or _native()).combine(y, route.rows, route.slots, weights)
     if out is not None:
         return out
     if weights is None:
@@ -1080,7 +1106,7 @@ def _matmul(a, w, cols, offsets, matrices, out, workspace, stream, bs):
     if cols <= 0 or cols % 32:
         raise TraceError(f"cols must be a multiple of 32: {cols}")
     if out is None and workspace is None and stream is None and not (DEBUG and offsets is not None):
-        got = (_bind or binding()).matmul(bs, cols, matrices, offsets, a.codes, a.scales,
+        got = (_bind or _native()).matmul(bs, cols, matrices, offsets, a.codes, a.scales,
                                           a.gscale if bs == 16 else None, w.codes, w.scales,
                                           w.gscale if bs == 16 else None)
         if got is not None:

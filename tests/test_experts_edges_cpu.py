@@ -6,6 +6,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 import pytest
 import torch
@@ -110,3 +111,31 @@ def test_the_module_belongs_to_its_torch(tmp_path, monkeypatch):
     monkeypatch.setattr(ops, "_bind", None)
     with pytest.raises(ops.TraceError, match="has not been built"):
         ops.binding()
+
+
+def test_calls_without_the_module(monkeypatch):
+    """A warning, once, and the calls go on to their own checks; binding() says
+    what is missing, and finds the module once it is there."""
+    monkeypatch.setattr(ops, "_bind", None)
+    with monkeypatch.context() as m:
+        m.setattr(ops._build, "binding_path", lambda: os.path.join(HERE, "no_such_module.so"))
+        with pytest.raises(ops.TraceError, match="has not been built"):
+            ops.binding()
+        ids = torch.zeros(3, 2, dtype=torch.int32)
+        route = ops.MoeRoute(torch.zeros(6, dtype=torch.int64), ids, ids.view(-1))
+        x, y, w = torch.zeros(3, 32).bfloat16(), torch.zeros(6, 32).bfloat16(), torch.zeros(3, 2)
+        a = ops.Capture(torch.zeros(128, dtype=torch.uint8), None, torch.zeros(4, 4, dtype=torch.uint8),
+                        torch.ones(1))
+        calls = (lambda: ops.moe_sort(ids, 4), lambda: ops.moe_dispatch(x, route),
+                 lambda: ops.moe_combine(y, route, w), lambda: ops.fp4_matmul(a, a))
+        with pytest.warns(RuntimeWarning, match="has not been built"):
+            with pytest.raises(ops.TraceError, match="must be CUDA tensors"):
+                calls[0]()
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            for call in calls:
+                with pytest.raises(ops.TraceError, match="must be CUDA tensors"):
+                    call()
+        with pytest.raises(ops.TraceError, match="has not been built"):
+            ops.binding()
+    assert ops.binding().sort(ids, 4) is None and ops._bind is ops.binding()
