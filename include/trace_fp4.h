@@ -531,7 +531,10 @@ int trace_moe_combine_bwd(const uint16_t* grad_out, const uint16_t* y, int64_t t
  *               (code * block scale of a at r, k) *
  *               (code * block scale of w at g * n + j, k)),
  * g the group of row r (trace_mx_matmul: E8M0 scales and no global scales).
- * The terms are exact and the sum is held in fp32.
+ * The sum is held in fp32.  The terms are exact: of NVFP4 always, of MXFP4 where
+ * they fit fp32.  (Two of its scales may multiply to less than 2^-149, and such
+ * a term is rounded to a multiple of that; or to more than 2^127, and a sum that
+ * passes fp32's largest number is infinite or NaN.)
  *   a_*     : a capture of [rows, cols] with num_groups groups (offsets as
  *             everywhere; NULL for one group).
  *   w_*     : a capture of num_matrices matrices [n, cols] stacked by rows,

@@ -169,3 +169,31 @@ def test_status_of_products_from_several_threads():
     for t in threads:
         t.join()
     assert len(said) == 4 * 51 and all(said)
+
+
+@pytest.mark.parametrize("rows,n,cols", [(20, 24, 64), (5, 256, 1024), (300, 264, 320)])
+@pytest.mark.parametrize("ea,ew", [(0xF0, 0x0E), (0xFE, 0x00), (0x00, 0xFE), (0x40, 0x3F), (0x3C, 0x3B),
+                                   (0xC0, 0xC4), (0xFE, 0xFE), (0x00, 0x00), (0x7F, 0x05), (0x20, 0x20)])
+def test_mx_scales_at_the_ends_of_their_range(way, rows, n, cols, ea, ew):
+    """Block scales of 2^-127 to 2^127: large against small ones with ordinary
+    sums, sums in and below bf16's subnormal range, and sums past its end.  A block's
+    two scales move by +-2 around ea and ew in opposite directions, so that the
+    terms of a sum are of like size."""
+    g = _gen(ea * 256 + ew)
+    c = cols // 32
+    codes = lambda r: torch.randint(0, 256, (r, cols // 2), generator=g, dtype=torch.uint8)  # noqa: E731
+    step = torch.randint(-2, 3, (c,), generator=g)
+    sa = (torch.full((rows, c), ea) + step).clamp(0, 254).to(torch.uint8)
+    sw = (torch.full((n, c), ew) - step).clamp(0, 254).to(torch.uint8)
+    a = ops.MxCapture(codes(rows).to(DEV), None, sa.to(DEV))
+    w = ops.MxCapture(codes(n).to(DEV), None, sw.to(DEV))
+    out = ref.f64(ops.mx_matmul(a, w))
+    va = ref.operand(a.codes.cpu().numpy(), sa.numpy(), rows, cols, "mxfp4")
+    vw = ref.operand(w.codes.cpu().numpy(), sw.numpy(), n, cols, "mxfp4")
+    exact, mag = ref.product(va, vw, None, None, [0, rows], n)
+    # as product_bound, and a term below fp32's normal range is off by one unit of its
+    # subnormals, 2^-149
+    bound = ref.product_bound(exact, mag, cols) + cols * 2.0 ** -149
+    over, inside = np.abs(exact) - bound > 3.4e38, mag < 3.3e38
+    assert np.all(np.abs(out - exact)[inside] <= bound[inside])
+    assert np.all(~np.isfinite(out[over]))
