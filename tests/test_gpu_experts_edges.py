@@ -197,3 +197,44 @@ def test_mx_scales_at_the_ends_of_their_range(way, rows, n, cols, ea, ew):
     over, inside = np.abs(exact) - bound > 3.4e38, mag < 3.3e38
     assert np.all(np.abs(out - exact)[inside] <= bound[inside])
     assert np.all(~np.isfinite(out[over]))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tiled", [False, True])
+@pytest.mark.parametrize("rows,n,cols,counts", [
+    (1, 4096, 4096, None), (29, 300, 8224, None), (140, 136, 4128, None), (700, 520, 4160, None),
+    (600, 389, 4096, None), (64, 256, 4096, [20, 1, 43]), (900, 256, 4128, [300, 2, 598])])
+def test_no_term_of_a_long_sum_is_lost(way, fmt, tiled, rows, n, cols, counts):
+    """Codes of -1, 0 and 1 and block scales that are powers of two and cancel
+    between the operands: sums of whole numbers up to 256, exact in fp32 in any
+    order and in bf16, so a lost or doubled term shows."""
+    g = _gen(rows + n + cols)
+    bs = 16 if fmt == "nvfp4" else 32
+    matrices = 1 if counts is None else len(counts)
+    bounds = [0, rows] if counts is None else np.concatenate([[0], np.cumsum(counts)]).tolist()
+
+    def draw(r):
+        v = torch.randint(-1, 2, (r, cols), generator=g)
+        v[torch.rand(r, cols, generator=g) < 0.4] = 0
+        nib = torch.where(v > 0, 2, torch.where(v < 0, 10, 0)).to(torch.uint8)
+        return v.float().to(DEV), (nib[:, 0::2] | nib[:, 1::2] << 4).reshape(-1).contiguous().to(DEV)
+
+    (va, ca), (vw, cw) = draw(rows), draw(matrices * n)
+    p = torch.randint(-3, 4, (cols // bs,), generator=g)
+    one, unit = (0x38, 8) if fmt == "nvfp4" else (127, 1)
+    sa = (one + unit * p).to(torch.uint8).expand(rows, -1).contiguous()
+    sw = (one - unit * p).to(torch.uint8).expand(matrices * n, -1).contiguous()
+    if tiled:
+        sa, sw = (torch.from_numpy(ref.tile(s.numpy(), 0xFF)) for s in (sa, sw))
+    sa, sw = sa.to(DEV), sw.to(DEV)
+    offs = None if counts is None else torch.tensor(bounds, device=DEV)
+    if fmt == "nvfp4":
+        one = torch.ones(matrices, device=DEV)
+        out = ops.fp4_matmul(ops.Capture(ca, None, sa, one, offs), ops.Capture(cw, None, sw, one), cols)
+    else:
+        out = ops.mx_matmul(ops.MxCapture(ca, None, sa), ops.MxCapture(cw, None, sw), cols, offs, matrices)
+    for e in range(matrices):
+        lo, hi = bounds[e], bounds[e + 1]
+        want = va[lo:hi].double() @ vw[e * n:(e + 1) * n].double().t()
+        assert want.numel() == 0 or want.abs().max() <= 256
+        assert torch.equal(out[lo:hi].double(), want)
