@@ -602,7 +602,9 @@ __device__ __forceinline__ void copy_scales(const ScaleSrc& s, const uint8_t* ba
 // 2446 and 117 with 2447, 67 with 2448; one column at a time 136.  65536 x 1534 x
 // 2048, 32 experts: 128 and 140; 4099 x 4001 x 4096, where the stores come beside
 // the next tile's products: 37.6 and 36.6).  Kernels of their own, because the
-// registers of both would not fit one.
+// registers of both would not fit one: as it is, all of them use up to 128 without
+// spills but the NVFP4 pairs with rows not in whole 16 bytes, which spill 8 bytes
+// (28 of loads).
 // ---------------------------------------------------------------------------
 struct MmMaps {
   CUtensorMap a, w;    // codes
