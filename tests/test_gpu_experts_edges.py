@@ -238,3 +238,23 @@ def test_no_term_of_a_long_sum_is_lost(way, fmt, tiled, rows, n, cols, counts):
         want = va[lo:hi].double() @ vw[e * n:(e + 1) * n].double().t()
         assert want.numel() == 0 or want.abs().max() <= 256
         assert torch.equal(out[lo:hi].double(), want)
+
+
+def test_calls_under_inference_mode(way):
+    """The chain of a rollout without autograd, on tensors that have no version, and
+    on a route of theirs outside of it."""
+    x = torch.randn(37, 64, generator=_gen(2)).bfloat16().to(DEV)
+    w = torch.rand(37, 3, generator=_gen(3)).to(DEV)
+    plain = _route(37, 3, 5, 1)
+    want = ops.moe_combine(ops.moe_dispatch(x, plain), plain, w)
+    with torch.inference_mode():
+        route = _route(37, 3, 5, 1)
+        out = ops.moe_combine(ops.moe_dispatch(x, route), route, w)
+        a, b = ops.capture(x), ops.capture(x[:8].contiguous())
+        product = ops.fp4_matmul(a, b)
+    assert out.is_inference() and torch.equal(out, want)
+    assert torch.equal(product, ops.fp4_matmul(a, b))
+    assert torch.equal(ops.moe_combine(ops.moe_dispatch(x, route), route, w), want)
+    with torch.no_grad():
+        xg = x.clone().requires_grad_()
+        assert not ops.moe_combine(ops.moe_dispatch(xg, plain), plain, w).requires_grad
